@@ -348,6 +348,95 @@ cb_status cb_paged_attention_no_alloc(void* out, const void* q, void* k_cache, v
  */
 cb_status cb_no_alloc_read_error_word(int32_t* h_error, void* stream);
 
+/* ---- 8-bit paged cache -------------------------------------------------- */
+
+/*
+ * The 8-bit cache holds K and V as e4m3 values with one power-of-two scale per row (the K or V
+ * of one token and KV head): half the bytes of a bf16 cache, and so half the decode stream
+ * ("Continuous batching mechanics", d9bl.com: decode is bound by the bytes of the cache, and
+ * the cache bounds how many requests run). Layouts, row-major and contiguous:
+ *   k_cache, v_cache   [num_blocks, block_size, Hkv, D]   e4m3, one byte each
+ *   k_scale, v_scale   [num_blocks, block_size, Hkv]      e8m0: byte c stands for 2^(c - 127)
+ * A row x[D] is stored with the least exponent e >= -126 for which max |x| <= 448 * 2^e over
+ * its finite elements (e = 0 where they are all zero), as x / 2^e rounded to the nearest e4m3
+ * value (ties to even). Infinities are stored as the largest magnitude, 448 scales; a NaN stays
+ * a NaN. The element read back is its e4m3 value times 2^e: at most 2^-4 of its magnitude off,
+ * or 2^-10 scales for elements below 2^-6 scales. Every scale product is exact.
+ * Supported: head_dim 64 or 128; all pointers 16-byte aligned.
+ */
+
+/*
+ * cb_write_kv_q8 -- cb_write_kv into the 8-bit cache: every row of the step with
+ * slot_mapping[t] >= 0 is quantised as above into its slot, its scale beside it.
+ *
+ * k_new, v_new: device [T, Hkv, D] in `dtype` (CB_F32 or CB_BF16); the four cache arrays are
+ * written; slot_mapping, error_word and stream as for cb_write_kv. Two tokens with the same
+ * non-negative slot race: the slot then holds an unspecified mixture of the two.
+ */
+cb_status cb_write_kv_q8(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                         void* k_scale, void* v_scale, const int64_t* slot_mapping,
+                         int32_t num_tokens, int32_t num_blocks, int32_t block_size,
+                         int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                         int32_t* error_word, void* stream);
+
+/*
+ * cb_read_kv_q8 -- rows of the 8-bit cache in full precision: k_out[t], v_out[t] become the
+ * rows at slot slot_mapping[t] (a slot may occur more than once). A row whose slot is negative
+ * is left as it was; one past the pool too, and CB_DEVERR_SLOT is recorded.
+ *
+ * k_out, v_out: device [T, Hkv, D] in `dtype`, written: exactly in CB_F32, and in CB_BF16
+ * (whose 8-bit significand and range hold every value of scale 2^-117 or more). Scale byte 0
+ * reads as 2^-127 and 255 as NaN. Asynchronous on `stream`.
+ */
+cb_status cb_read_kv_q8(const void* k_cache, const void* v_cache, const void* k_scale,
+                        const void* v_scale, const int64_t* slot_mapping, void* k_out,
+                        void* v_out, int32_t num_tokens, int32_t num_blocks, int32_t block_size,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                        int32_t* error_word, void* stream);
+
+/*
+ * cb_workspace_size_q8 -- bytes of device workspace cb_paged_attention_q8 needs for steps of up
+ * to these sizes. chunk_kv_tokens: the most KV positions (sum of seq_lens) that the requests
+ * with q_len > 1 of one step have together; 0 for steps of decode rows only (and for fp32
+ * steps, which need no scratch for them). Long query runs (more than 64 query columns, tokens
+ * times the group size) are computed from a bf16 copy of their requests' pages, which lives
+ * there for the step: 4 Hkv D bytes a position.
+ * The workspace is initialised with cb_workspace_init and its error word read with
+ * cb_read_error_word, as cb_paged_attention's.
+ */
+size_t cb_workspace_size_q8(int32_t num_requests, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                            int64_t chunk_kv_tokens);
+
+/*
+ * cb_paged_attention_q8 -- the step of cb_paged_attention over an 8-bit cache.
+ *
+ * With k_new, the step first quantises its new rows into their slots exactly as cb_write_kv_q8
+ * does; attention reads them back from the cache, so a row's own position takes part with its
+ * stored value. Then, with K_p and V_p the stored values (e4m3 times scale),
+ *     out[t, h] = sum_p softmax_p(scale * <q[t, h], K_p[g]>) * V_p[g]
+ * over the positions of cb_paged_attention, accumulated in fp32 and rounded to the dtype of q.
+ * Arguments, metadata, host mirrors, errors and flags are cb_paged_attention's (dtype is that
+ * of q, out, k_new and v_new; CB_FLAG_PORTABLE_ONLY is honoured), with the two scale arrays
+ * after the caches. Scale bytes of attended rows lie in 1 .. 254.
+ *
+ * Block sizes that are multiples of 16 run on the tensor cores; smaller ones on the CUDA cores.
+ * CB_ERR_WORKSPACE where the workspace is smaller than cb_workspace_size_q8() says for the
+ * step's sizes, chunk_kv_tokens included. Calls that share a workspace are ordered on one
+ * stream; so a captured call and its replays keep the workspace to themselves.
+ */
+cb_status cb_paged_attention_q8(void* out, const void* q, void* k_cache, void* v_cache,
+                                void* k_scale, void* v_scale, const void* k_new,
+                                const void* v_new, const int64_t* slot_mapping,
+                                const int32_t* query_start_loc, const int32_t* seq_lens,
+                                const int32_t* block_table, int32_t block_table_stride,
+                                const int32_t* h_query_start_loc, const int32_t* h_seq_lens,
+                                int32_t num_requests, int32_t num_tokens, int32_t num_blocks,
+                                int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, float scale, int32_t sliding_window,
+                                int32_t dtype, uint32_t flags, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 /* ---- diagnostics (no effect on results) -------------------------------- */
 
 /* Number of kernels the library has launched in this process: of kernel id

@@ -75,6 +75,11 @@ _SIGNATURES = {
         _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
         _i32, _i32, _i32, _i32, _i32, _i32, _i32, ctypes.c_float, _i32, _i32, ctypes.c_uint32,
         _vp]),
+    "cb_write_kv_q8": (ctypes.c_int, [_vp] * 7 + [_i32] * 6 + [_vp, _vp]),
+    "cb_read_kv_q8": (ctypes.c_int, [_vp] * 7 + [_i32] * 6 + [_vp, _vp]),
+    "cb_workspace_size_q8": (ctypes.c_size_t, [_i32] * 6 + [ctypes.c_int64]),
+    "cb_paged_attention_q8": (ctypes.c_int, [_vp] * 12 + [_i32, _vp, _vp] + [_i32] * 7 + [
+        ctypes.c_float, _i32, _i32, ctypes.c_uint32, _vp, ctypes.c_size_t, _vp]),
     "cb_launch_count": (ctypes.c_longlong, [ctypes.c_int]),
     "cb_num_kernels": (ctypes.c_int, []),
     "cb_kernel_name": (ctypes.c_char_p, [ctypes.c_int]),
@@ -334,6 +339,183 @@ def no_alloc_read_error_word(stream=None) -> int:
     if status not in (0, 6):
         _check(status)
     return int(word.value)
+
+
+# ---------------------------------------------------------------- 8-bit paged cache
+
+
+def _need(t, name, shape, kinds, device=None):
+    """A contiguous CUDA tensor of the given shape and one of the given dtypes."""
+    if t.dtype not in kinds:
+        raise CbError(1, f"{name}: dtype {t.dtype}, not one of {', '.join(map(str, kinds))}")
+    if t.shape != shape:
+        raise CbError(1, f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise CbError(1, f"{name} must be contiguous")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise CbError(1, f"{name} must be on {'a CUDA device' if device is None else device}")
+
+
+def _kinds():
+    global _E4M3, _E8M0, _I32, _I64, _FLOATS
+    import torch
+
+    _E4M3 = (torch.float8_e4m3fn, torch.uint8)
+    _E8M0 = (torch.float8_e8m0fnu, torch.uint8)
+    _I32 = (torch.int32,)
+    _I64 = (torch.int64,)
+    _FLOATS = (torch.bfloat16, torch.float32)
+
+
+_E4M3 = _E8M0 = _I32 = _I64 = _FLOATS = None
+
+
+def _need_cache_q8(k_cache, v_cache, k_scale, v_scale, Hkv, D, device):
+    """Checks the four arrays of an 8-bit cache; returns (num_blocks, block_size)."""
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[2] != Hkv or shape[3] != D:
+        raise CbError(1, f"k_cache: shape {tuple(shape)}, not [num_blocks, block_size, {Hkv}, {D}]")
+    _need(k_cache, "k_cache", shape, _E4M3, device)
+    _need(v_cache, "v_cache", shape, _E4M3, device)
+    _need(k_scale, "k_scale", shape[:3], _E8M0, device)
+    _need(v_scale, "v_scale", shape[:3], _E8M0, device)
+    return shape[0], shape[1]
+
+
+def _on(device):
+    """The guard under which a call for tensors on ``device`` runs: the library launches on the
+    current device."""
+    import contextlib
+
+    import torch
+
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _stream_on(stream, device):
+    if stream is not None:
+        return _stream(stream)
+    import torch
+
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _rows_q8(fn, a, b, rows, cache, slot_mapping, error_word, stream):
+    if _E4M3 is None:
+        _kinds()
+    k = rows[0]
+    if k.dim() != 3:
+        raise CbError(1, f"rows must be [T, Hkv, D], not {tuple(k.shape)}")
+    T, Hkv, D = k.shape
+    dev = k.device
+    _need(rows[0], a, k.shape, _FLOATS)
+    _need(rows[1], b, k.shape, (k.dtype,), dev)
+    NB, BS = _need_cache_q8(*cache, Hkv, D, dev)
+    _need(slot_mapping, "slot_mapping", (T,), _I64, dev)
+    if error_word is not None:
+        _need(error_word, "error_word", error_word.shape, _I32, dev)
+    c = [t.data_ptr() for t in cache]
+    r = [t.data_ptr() for t in rows]
+    ptrs = (*r, *c, slot_mapping.data_ptr()) if fn == "cb_write_kv_q8" else (
+        *c, slot_mapping.data_ptr(), *r)
+    with _on(dev):
+        _check(getattr(lib(), fn)(*ptrs, T, NB, BS, Hkv, D, _dtype_code(k), _ptr(error_word),
+                                  _stream_on(stream, dev)))
+
+
+def write_kv_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping, error_word=None,
+                stream=None):
+    """Quantise k_new/v_new [T, Hkv, D] (bf16 or fp32) into the 8-bit caches [NB, BS, Hkv, D]
+    (float8_e4m3fn) and their scales [NB, BS, Hkv] (float8_e8m0fnu) at slot_mapping [T].
+    uint8 tensors are taken for either as well (see cb_write_kv_q8 in include/cb.h)."""
+    _rows_q8("cb_write_kv_q8", "k_new", "v_new", (k_new, v_new),
+             (k_cache, v_cache, k_scale, v_scale), slot_mapping, error_word, stream)
+
+
+def read_kv_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out, error_word=None,
+               stream=None):
+    """k_out/v_out [T, Hkv, D] (bf16 or fp32) = the 8-bit caches' rows at slot_mapping [T]
+    (rows of negative slots stay as they are; see cb_read_kv_q8 in include/cb.h)."""
+    _rows_q8("cb_read_kv_q8", "k_out", "v_out", (k_out, v_out),
+             (k_cache, v_cache, k_scale, v_scale), slot_mapping, error_word, stream)
+
+
+def workspace_size_q8(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                      chunk_kv_tokens=0) -> int:
+    return int(lib().cb_workspace_size_q8(num_requests, num_tokens, num_q_heads, num_kv_heads,
+                                          head_dim, block_size, chunk_kv_tokens))
+
+
+def alloc_workspace_q8(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
+                       chunk_kv_tokens=0, device="cuda"):
+    """Allocate (with torch) and zero a workspace of cb_workspace_size_q8 bytes."""
+    import torch
+
+    n = workspace_size_q8(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                          block_size, chunk_kv_tokens)
+    return torch.zeros((n + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def _step_checks(out, q, Hkv, query_start_loc, seq_lens, block_table, h_query_start_loc,
+                 h_seq_lens, k_new, v_new, slot_mapping, workspace):
+    """The tensors every step takes; returns (T, Hq, D, R, stride, host mirrors, device)."""
+    if _E4M3 is None:
+        _kinds()
+    if q.dim() != 3:
+        raise CbError(1, f"q must be [T, Hq, D], not {tuple(q.shape)}")
+    T, Hq, D = q.shape
+    dev = q.device
+    _need(q, "q", q.shape, _FLOATS)
+    kinds = (q.dtype,)
+    _need(out, "out", q.shape, kinds, dev)
+    R = seq_lens.shape[0]
+    _need(seq_lens, "seq_lens", (R,), _I32, dev)
+    _need(query_start_loc, "query_start_loc", (R + 1,), _I32, dev)
+    if block_table.dim() != 2:
+        raise CbError(1, "block_table must be [R, stride]")
+    stride = block_table.shape[1]
+    _need(block_table, "block_table", (R, stride), _I32, dev)
+    if k_new is not None:
+        if v_new is None or slot_mapping is None:
+            raise CbError(1, "k_new given without v_new or slot_mapping")
+        _need(k_new, "k_new", (T, Hkv, D), kinds, dev)
+        _need(v_new, "v_new", (T, Hkv, D), kinds, dev)
+        _need(slot_mapping, "slot_mapping", (T,), _I64, dev)
+    if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise CbError(4, f"workspace must be contiguous, on {dev}")
+    hq, hs = _host_i32(h_query_start_loc), _host_i32(h_seq_lens)
+    if hq.shape != (R + 1,) or hs.shape != (R,):
+        raise CbError(2, "host mirrors must have R+1 and R entries")
+    return T, Hq, D, R, stride, hq, hs, dev
+
+
+def paged_attention_q8(out, q, k_cache, v_cache, k_scale, v_scale, query_start_loc, seq_lens,
+                       block_table, h_query_start_loc, h_seq_lens, workspace, *, scale=0.0,
+                       sliding_window=0, k_new=None, v_new=None, slot_mapping=None, flags=0,
+                       stream=None):
+    """paged_attention over an 8-bit cache (see cb_paged_attention_q8 in include/cb.h).
+
+    out, q: [T, Hq, D] bf16 or fp32; caches [NB, BS, Hkv, D] float8_e4m3fn and scales
+    [NB, BS, Hkv] float8_e8m0fnu (or uint8); the step's k_new/v_new are quantised into their
+    slots first. workspace: alloc_workspace_q8.
+    """
+    Hkv = k_cache.shape[2] if k_cache.dim() == 4 else 0
+    T, Hq, D, R, stride, hq, hs, dev = _step_checks(
+        out, q, Hkv, query_start_loc, seq_lens, block_table, h_query_start_loc, h_seq_lens, k_new,
+        v_new, slot_mapping, workspace)
+    NB, BS = _need_cache_q8(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev)
+    with _on(dev):
+        _check(lib().cb_paged_attention_q8(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_new),
+            _ptr(v_new), _ptr(slot_mapping),
+            query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), stride,
+            hq.ctypes.data, hs.ctypes.data, R, T, NB, BS, Hq, Hkv, D, float(scale),
+            int(sliding_window), _dtype_code(q), int(flags), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
+    return out
 
 
 def launch_count(kernel: int = -1) -> int:

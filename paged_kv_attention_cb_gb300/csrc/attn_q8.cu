@@ -1,0 +1,962 @@
+// Attention over the 8-bit paged cache (q8.cuh): split-KV kernel for decode rows and short
+// runs of query tokens, and a portable CUDA-core kernel for the shapes it does not cover.
+//
+// Split kernel. What it computes is the per-block pseudocode of "Continuous Batching"
+// (languisher.top), section "Extension: the vLLM v1 implementation", on rows that stand in the
+// cache as y * 2^e. With the K row's exponent ek, the V row's ev and column c (a query token
+// and head of the KV head's group):
+//     s_j = scale_log2 <q_c, yk_j> 2^ek_j          (log2 units)
+//     out_c = sum_j 2^s_j 2^ev_j yv_j / sum_j 2^s_j
+// so both scales leave the contractions: 2^ek multiplies a score, ev is added to the exponent
+// of the weight that multiplies V.
+//
+// Decode streams every attended byte once and is HBM-bound, now at half the bytes of a bf16
+// cache; the kernel must turn each byte into a tensor-core operand at ~44 bytes/ns per SM.
+//
+// * Partition. The (request, tile of query tokens) items' 16-key blocks are numbered in
+//   request order and CTA b of C takes blocks [b U / C, (b + 1) U / C): equal bytes per CTA.
+//   An item inside one CTA is written directly; a piece of a longer one becomes a partial row
+//   that the merge kernel joins (merge.h).
+// * Staging. A producer warp brings each block (16 keys, up to 8 KV heads, K and V) with two
+//   swizzled tensor copies and its scales with two bulk copies into a ring of stages.
+// * Operands. e4m3 is exact in fp16, so the contractions are fp16 mma.sync with fp32
+//   accumulation, and the conversion is one instruction per pair (cvt.f16x2.e4m3x2). q is
+//   scaled per row by a power of two to a largest magnitude in [2^13, 2^14): a bf16 row is
+//   then exact down to 2^-38 of its largest element, and an fp32 row is the sum of two fp16
+//   rows to 2^-22. Weights are fp16 (bf16 queries: 11 bits, finer than the bf16 the output is
+//   rounded to) or the sum of two fp16 (fp32 queries), scaled to at most 2^14.
+// * Layout. Keys are the M = 16 rows of both products' A operand side, columns the N = 8.
+//   The contraction index may be permuted freely, so a lane takes its operands from whole
+//   16-byte pieces of the staged rows: for S^T = K Q^T lane (g, t) holds d = D/4 t ..
+//   D/4 t + D/4 - 1 of keys g and g + 8; for O^T = V^T P^T it holds d = D/8 g .. of keys
+//   2t, 2t+1, 2t+8, 2t+9, pairs of keys interleaved bytewise (prmt) before the conversion.
+//   O then has a lane's outputs contiguous in d: 32-byte stores.
+// * Softmax. Two running maxima per column, of s_j (for the sum) and of s_j + ev_j (for the
+//   weights), because rows of very different V scales may meet: with one maximum a large
+//   scale on an unattended key would push the attended ones' weights under fp16's range. Both
+//   are raised only when exceeded by more than 2^8, which a warp vote finds without the
+//   cross-lane maximum. Statistics, sums and outputs are fp32.
+// * Warps. KW warps share a KV head and take the blocks in turn, each with its own state;
+//   they join through shared memory at the end of an item's piece. At 8 heads and two warps
+//   each, one warp has ~1400 cycles per 16-key block at the HBM rate.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <float.h>
+
+#include "cb.h"
+#include "common.cuh"
+#include "launch.h"
+#include "q8.cuh"
+#include "q8.h"
+#include "sm100_ptx.cuh"
+
+namespace cb {
+
+namespace {
+
+constexpr int kKB = kQ8KeyBlock;
+constexpr float kNoMax = -1e30f;     // running maximum before any key (finite: no inf - inf)
+constexpr float kRaise = 8.f;        // the maxima are raised when exceeded by more than 2^8
+constexpr float kWeightLog2 = 6.f;   // weights are at most 2^(8 + 6), inside fp16's range
+constexpr int kMaxQueue = 2;         // pieces handed ahead to the consumers
+
+struct Q8Piece {
+  int t0;      // packed query row of the item's first token (-1: no more pieces)
+  int ntok;
+  int n;       // key blocks of this piece
+  int kb0;     // first of them
+  int pos0;    // position of the first token
+  int slot;    // partial slot: 2 b for CTA b's first piece, 2 b + 1 for its last
+  int direct;  // the whole item lies in this CTA
+};
+
+struct Q8Smem {
+  uint64_t full[kQ8MaxStages];
+  uint64_t empty[kQ8MaxStages];
+  uint64_t pfull[kMaxQueue];
+  uint64_t pempty[kMaxQueue];
+  uint64_t xfull[16];   // exchange slot written by warp (key warp, head)
+  uint64_t xempty[16];  // and read
+  Q8Piece piece[kMaxQueue];
+  int abort_flag;
+};
+
+// Position of key row i (0 .. 15) of a tile within its block. For D 64 (64-byte rows) the low
+// two bits change places, so that the rows of a V fragment (2t, t = 0 .. 3) fall on both
+// halves of the banks.
+template <int D>
+CB_DEV int key_of_row(int i) {
+  return D == 64 ? ((i & ~3) | ((i & 1) << 1) | ((i & 2) >> 1)) : i;
+}
+
+// Byte offset of 16-byte chunk c of staged row `row` (rows of D bytes, copied with the 128- or
+// 64-byte swizzle).
+template <int D>
+CB_DEV uint32_t row_chunk(int row, int c) {
+  if constexpr (D == 128) return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4));
+  return (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+}
+
+CB_DEV void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+CB_DEV uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The pair's remainder after rounding to fp16, as fp16.
+CB_DEV uint32_t pack_f16x2_rest(uint32_t rounded, float lo, float hi) {
+  const float2 r = float2_of_f16x2(rounded);
+  return pack_f16x2(lo - r.x, hi - r.y);
+}
+
+CB_DEV uint32_t f16x2_lo(uint32_t w) { return f16x2_of_e4m3x2((uint16_t)w); }
+CB_DEV uint32_t f16x2_hi(uint32_t w) { return f16x2_of_e4m3x2((uint16_t)(w >> 16)); }
+
+CB_DEV uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+CB_DEV uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+
+CB_DEV int lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return (int)v;
+}
+
+// First key block of a run of ntok tokens starting at position pos0, and how many it attends.
+CB_DEV int first_key(int pos0, int window) { return window > 0 ? max(0, pos0 - window + 1) : 0; }
+CB_DEV int blocks_of(int pos0, int ntok, int window) {
+  return (pos0 + ntok - 1) / kKB - first_key(pos0, window) / kKB + 1;
+}
+
+// CTA that owns global block u (ranges [b U / C, (b + 1) U / C)).
+CB_DEV int owner_of(long long u, long long U, int C) {
+  return (int)(((u + 1) * (long long)C + U - 1) / U) - 1;
+}
+
+}  // namespace
+
+// NB column blocks of 8; F32: fp32 queries and outputs (operands split into two fp16 parts).
+template <int D, int NB, bool F32>
+__global__ void __launch_bounds__((NB == 1 ? 16 : 8) * 32 + 32, 1)
+q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ Q8Args p) {
+  constexpr int kKS = D / 16;          // contraction steps over head_dim; output tiles of 16
+  constexpr int kSplit = F32 ? 2 : 1;  // fp16 parts of q and of the weights
+  constexpr int kXRegs = 16;           // outputs per exchange round
+  extern __shared__ __align__(1024) uint8_t smem_dyn[];
+  uint8_t* base = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
+  const int HB = p.heads_per_cta, KW = p.key_warps, Hkv = p.a.num_kv_heads;
+  const int box_bytes = HB * kKB * D;      // K (or V) of one block
+  const int stage_bytes = 2 * box_bytes;
+  const int scale_bytes = kKB * Hkv;       // K (or V) scales of one block, every head
+  uint8_t* stages = base;
+  uint8_t* scales = stages + p.stages * stage_bytes;
+  float* xchg = reinterpret_cast<float*>(scales + p.stages * 2 * scale_bytes);
+  constexpr int kXFloats = (6 * NB + kXRegs) * 32;
+  Q8Smem& sm = *reinterpret_cast<Q8Smem*>(xchg + (KW - 1) * HB * kXFloats);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.x;
+  const int hg = blockIdx.y;
+  const int nwarps = HB * KW;  // consumer warps; the next one is the producer
+  const int W = p.a.sliding_window;
+  const int TT = p.tile_tokens;
+  const long long U = p.total_units;
+  const int C = p.num_ctas;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], HB);
+    }
+    for (int s = 0; s < kMaxQueue; ++s) {
+      mbar_init(&sm.pfull[s], 1);
+      mbar_init(&sm.pempty[s], nwarps);
+    }
+    for (int s = 0; s < 16; ++s) {
+      mbar_init(&sm.xfull[s], 1);
+      mbar_init(&sm.xempty[s], 1);
+    }
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  // scales of a block that was never copied (a page id out of range) read as the smallest
+  for (int i = threadIdx.x; i < p.stages * 2 * scale_bytes / 4; i += blockDim.x)
+    reinterpret_cast<uint32_t*>(scales)[i] = 0u;
+  fence_proxy_async_smem();
+  if (warp == nwarps && lane == 0) {
+    prefetch_tensormap(&tmap_k);
+    prefetch_tensormap(&tmap_v);
+  }
+  grid_dependency_wait();
+  allow_dependent_launch();
+  __syncthreads();
+
+  int issued_blocks = 0;  // producer: copies issued (for the drain)
+  if (warp == nwarps) {
+    // =================================================== producer warp
+    const long long u_lo = (long long)b * U / C;
+    const long long u_hi = (long long)(b + 1) * U / C;
+    const uint64_t policy = l2_policy_evict_first();  // the stream is read once
+    const int BS = p.a.block_size;
+    bool ok = true;
+    int k = 0;  // pieces handed out
+    int i = 0;  // blocks issued
+    // Request metadata, 32 requests at a time (lane l: request wbase + l).
+    int wbase = -1, w_t = 0, w_q = 0, w_seq = 0;
+    auto load_window = [&](int r0) {
+      wbase = r0;
+      const int r = r0 + lane;
+      w_t = w_q = w_seq = 0;
+      if (r < p.a.num_requests) {
+        w_t = __ldg(p.a.query_start_loc + r);
+        w_q = __ldg(p.a.query_start_loc + r + 1) - w_t;
+        w_seq = __ldg(p.a.seq_lens + r);
+        if (w_q > p.max_q) w_q = 0;  // another kernel's rows
+      }
+    };
+    auto next_request = [&](int r) -> int {  // the next request with rows, from r on
+      while (r < p.a.num_requests) {
+        if (wbase < 0 || r - wbase >= 32 || r < wbase) load_window(r);
+        const unsigned m = __ballot_sync(0xffffffffu, w_q > 0 && wbase + lane >= r);
+        if (m) return wbase + __ffs(m) - 1;
+        r = wbase + 32;
+      }
+      return -1;
+    };
+    // the current item: its request's fields, its first block and its block count
+    int r = p.start[b].r, tile = p.start[b].tile;
+    long long u0 = p.start[b].u0;
+    int t0 = 0, qlen = 0, seq = 0, pos0 = 0, ntok = 0, nblk = 0, kb_lo = 0;
+    auto set_item = [&]() {
+      pos0 = seq - qlen + tile * TT;
+      ntok = min(TT, qlen - tile * TT);
+      kb_lo = first_key(pos0, W) / kKB;
+      nblk = blocks_of(pos0, ntok, W);
+    };
+    auto set_request = [&]() {
+      const int j = r - wbase;
+      t0 = __shfl_sync(0xffffffffu, w_t, j);
+      qlen = __shfl_sync(0xffffffffu, w_q, j);
+      seq = __shfl_sync(0xffffffffu, w_seq, j);
+    };
+    // page ids of key blocks kb .. kb + n - 1 of the request (lane l: block kb + l)
+    auto load_pages = [&](int rr, int kb, int n) -> int {
+      return lane < n ? __ldg(p.a.block_table + (long long)rr * p.a.bt_stride +
+                              bt_entry((kb + lane) * kKB / BS, p.a.ring_blocks))
+                      : 0;
+    };
+    bool more = r >= 0 && u_lo < u_hi;
+    int kb0 = 0, kb1 = 0, pages = 0;
+    if (more) {
+      load_window(r);
+      set_request();
+      set_item();
+      kb0 = kb_lo + (int)(u_lo - u0);
+      kb1 = kb_lo + (int)(min(u0 + nblk, u_hi) - u0);
+      pages = load_pages(r, kb0, min(32, kb1 - kb0));
+    }
+    while (more && ok) {
+      const int qs = k & 1;
+      if (k >= kMaxQueue &&
+          !mbar_wait_warp_or_abort(&sm.pempty[qs], (uint32_t)((k >> 1) - 1) & 1, &sm.abort_flag)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        Q8Piece& d = sm.piece[qs];
+        d.t0 = t0 + tile * TT;
+        d.ntok = ntok;
+        d.n = kb1 - kb0;
+        d.kb0 = kb0;
+        d.pos0 = pos0;
+        d.slot = 2 * b + (k > 0 ? 1 : 0);  // pieces between the two are direct
+        d.direct = owner_of(u0, U, C) == owner_of(u0 + nblk - 1, U, C);
+        mbar_arrive(&sm.pfull[qs]);
+      }
+      __syncwarp();
+      ++k;
+      // the item after this one, looked up once this piece's first copy is out
+      bool looked = false;
+      int nr = r, n_kb0 = 0, n_kb1 = 0;
+      const int cur_r = r, first = kb0, last = kb1;
+      const long long u_end = u0 + nblk;
+      for (int kb_base = first; kb_base < last && ok; kb_base += 32) {
+        const int n = min(32, last - kb_base);
+        const int cur = pages;
+        for (int j = 0; j < n; ++j) {
+          const int pg = __shfl_sync(0xffffffffu, cur, j);
+          const int s = i % p.stages;
+          if (i >= p.stages && !mbar_wait_warp_or_abort(&sm.empty[s], (uint32_t)((i / p.stages) - 1) & 1,
+                                                        &sm.abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (*reinterpret_cast<volatile int*>(&sm.abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            const int key0 = ((kb_base + j) * kKB) % BS;
+            uint8_t* st = stages + s * stage_bytes;
+            uint8_t* sc = scales + s * 2 * scale_bytes;
+            const bool page_ok = pg >= 0 && pg < p.a.num_blocks;
+            if (!page_ok) record_error(p.a.error_word, CB_DEVERR_BLOCK_ID);
+            mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(stage_bytes + (page_ok ? 2 * scale_bytes : 0)));
+            const int page = page_ok ? pg : p.a.num_blocks;  // past the pool: zeros
+            tma_load_4d_hint(st, &tmap_k, &sm.full[s], 0, key0, hg * HB, page, policy);
+            tma_load_4d_hint(st + box_bytes, &tmap_v, &sm.full[s], 0, key0, hg * HB, page, policy);
+            if (page_ok) {
+              const long long at = ((long long)pg * BS + key0) * Hkv;
+              bulk_load(sc, p.c.k_scale + at, (uint32_t)scale_bytes, &sm.full[s]);
+              bulk_load(sc + scale_bytes, p.c.v_scale + at, (uint32_t)scale_bytes, &sm.full[s]);
+            }
+          }
+          __syncwarp();
+          ++i;
+          if (j == 0) {
+            if (kb_base + 32 < last) {
+              pages = load_pages(cur_r, kb_base + 32, min(32, last - kb_base - 32));
+            } else if (!looked) {
+              looked = true;
+              more = u_end < u_hi;
+              if (more) {
+                if ((tile + 1) * TT < qlen) {
+                  ++tile;
+                } else {
+                  tile = 0;
+                  nr = next_request(r + 1);
+                  if (nr < 0) {
+                    more = false;
+                  } else {
+                    r = nr;
+                    set_request();
+                  }
+                }
+              }
+              if (more) {
+                u0 = u_end;
+                set_item();
+                n_kb0 = kb_lo;
+                n_kb1 = kb_lo + (int)(min(u0 + nblk, u_hi) - u0);
+                pages = load_pages(r, n_kb0, min(32, n_kb1 - n_kb0));
+              }
+            }
+          }
+        }
+      }
+      kb0 = n_kb0;
+      kb1 = n_kb1;
+    }
+    if (ok) {
+      const int qs = k & 1;
+      if (k >= kMaxQueue &&
+          !mbar_wait_warp_or_abort(&sm.pempty[qs], (uint32_t)((k >> 1) - 1) & 1, &sm.abort_flag))
+        ok = false;
+      if (ok && lane == 0) {
+        sm.piece[qs].t0 = -1;
+        mbar_arrive(&sm.pfull[qs]);
+      }
+    }
+    if (!ok && lane == 0) {
+      record_error(p.a.error_word, CB_DEVERR_TIMEOUT);
+      set_abort(&sm.abort_flag);
+    }
+    issued_blocks = i;
+  } else if (warp < nwarps) {
+    // =================================================== consumer warps
+    auto give_up = [&]() {
+      if (lane == 0) {
+        record_error(p.a.error_word, CB_DEVERR_TIMEOUT);
+        set_abort(&sm.abort_flag);
+      }
+    };
+    auto consume = [&]() {
+      const int hl = warp % HB, kw = warp / HB;
+      const int gid = lane >> 2, tq = lane & 3;
+      const int G = 1 << p.lg_group;
+      const int head = hg * HB + hl;  // KV head
+      const int Hq = p.a.num_q_heads;
+      const uint32_t stage0 = smem_u32(stages);
+      const uint32_t scale0 = smem_u32(scales) + head;
+      // rows of this lane's keys and chunks within a staged block
+      const int key_a = key_of_row<D>(gid), key_b = key_of_row<D>(gid + 8);
+      uint32_t k_off[2], v_off[4];
+      if constexpr (D == 128) {
+        k_off[0] = row_chunk<D>(hl * kKB + key_a, 2 * tq);  // the other chunk: address ^ 16
+        k_off[1] = row_chunk<D>(hl * kKB + key_b, 2 * tq);
+      } else {
+        k_off[0] = row_chunk<D>(hl * kKB + key_a, tq);
+        k_off[1] = row_chunk<D>(hl * kKB + key_b, tq);
+      }
+      int v_key[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v_key[j] = key_of_row<D>(2 * tq + (j & 1) + (j >> 1) * 8);
+        v_off[j] = box_bytes + (D == 128 ? row_chunk<D>(hl * kKB + v_key[j], gid)
+                                         : row_chunk<D>(hl * kKB + v_key[j], gid >> 1) + (gid & 1) * 8);
+      }
+      int i0 = 0;          // block index of the piece's first block
+      int xphase = 0;      // exchange rounds so far
+      for (int k = 0;; ++k) {
+        const int qs = k & 1;
+        if (!mbar_wait_warp_or_abort(&sm.pfull[qs], (uint32_t)(k >> 1) & 1, &sm.abort_flag)) {
+          give_up();
+          return;
+        }
+        const Q8Piece d = sm.piece[qs];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.pempty[qs]);
+        if (d.t0 < 0) break;
+
+        // ---- q: column 8 nb + gid, d = D/4 tq .. + D/4 - 1, as fp16 fragments
+        uint32_t qf[NB][kKS][2 * kSplit];
+        float cs0[NB], cs1[NB];  // score factors of columns 8 nb + 2 tq, + 1
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int col = 8 * nb + gid;
+          const int tok = col >> p.lg_group;
+          const bool live = tok < d.ntok;
+          const long long at =
+              ((long long)(d.t0 + tok) * Hq + head * G + (col & (G - 1))) * D + tq * (D / 4);
+          float x[D / 4];
+          if constexpr (F32) {
+            const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.a.q) + at);
+#pragma unroll
+            for (int e = 0; e < D / 16; ++e) {
+              const float4 v = live ? __ldg(src + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+              x[4 * e] = v.x;
+              x[4 * e + 1] = v.y;
+              x[4 * e + 2] = v.z;
+              x[4 * e + 3] = v.w;
+            }
+          } else {
+            const uint4* src =
+                reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) + at);
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e) {
+              const uint4 v = live ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                x[8 * e + 2 * c] = __uint_as_float(w[c] << 16);
+                x[8 * e + 2 * c + 1] = __uint_as_float(w[c] & 0xffff0000u);
+              }
+            }
+          }
+          uint32_t top = 0u;
+#pragma unroll
+          for (int e = 0; e < D / 4; ++e) top = max(top, finite_magnitude(x[e]));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int ex = top == 0u ? 13 : max((int)(top >> 23) - 127, -100);
+          const float up = __uint_as_float((uint32_t)(13 - ex + 127) << 23);
+          const float cs = p.a.scale_log2 * __uint_as_float((uint32_t)(ex - 13 + 127) << 23);
+          cs0[nb] = __shfl_sync(0xffffffffu, cs, 8 * tq);
+          cs1[nb] = __shfl_sync(0xffffffffu, cs, 8 * tq + 4);
+#pragma unroll
+          for (int ks = 0; ks < kKS; ++ks) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float lo = x[4 * ks + 2 * e] * up, hi = x[4 * ks + 2 * e + 1] * up;
+              qf[nb][ks][e] = pack_f16x2(lo, hi);
+              if constexpr (F32) qf[nb][ks][2 + e] = pack_f16x2_rest(qf[nb][ks][e], lo, hi);
+            }
+          }
+        }
+
+        float o[NB][kKS][4];
+        float m[NB][2], mw[NB][2], l[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int e = 0; e < kKS; ++e) o[nb][e][0] = o[nb][e][1] = o[nb][e][2] = o[nb][e][3] = 0.f;
+          m[nb][0] = m[nb][1] = mw[nb][0] = mw[nb][1] = kNoMax;
+          l[nb][0] = l[nb][1] = 0.f;
+        }
+        // keys every column attends: [all_lo, all_hi]; keys any column attends: [any_lo, any_hi]
+        const int any_lo = first_key(d.pos0, W), any_hi = d.pos0 + d.ntok - 1;
+        const int all_lo = first_key(any_hi, W), all_hi = d.pos0;
+
+        // this warp's blocks: global block indices congruent to kw modulo KW
+        for (int j = (kw - i0 % KW + KW) % KW; j < d.n; j += KW) {
+          const int i = i0 + j;
+          const int s = i % p.stages;
+          if (!mbar_wait_warp_or_abort(&sm.full[s], (uint32_t)(i / p.stages) & 1, &sm.abort_flag)) {
+            give_up();
+            return;
+          }
+          const uint32_t st = stage0 + s * stage_bytes;
+          const uint32_t sc = scale0 + s * 2 * scale_bytes;
+          const int key_base = (d.kb0 + j) * kKB;
+          const int ka = key_base + key_a, kb = key_base + key_b;
+
+          // ---- S^T = K Q^T
+          float sa[NB][4];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) sa[nb][0] = sa[nb][1] = sa[nb][2] = sa[nb][3] = 0.f;
+#pragma unroll
+          for (int half = 0; half < D / 64; ++half) {
+            const uint4 va = lds128(st + (k_off[0] ^ (half << 4)));
+            const uint4 vb = lds128(st + (k_off[1] ^ (half << 4)));
+            const uint32_t wa[4] = {va.x, va.y, va.z, va.w};
+            const uint32_t wb[4] = {vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t a[4] = {f16x2_lo(wa[e]), f16x2_lo(wb[e]), f16x2_hi(wa[e]), f16x2_hi(wb[e])};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                const uint32_t(&q)[2 * kSplit] = qf[nb][4 * half + e];
+                mma_f16_16816(sa[nb], a, q[0], q[1]);
+                if constexpr (F32) mma_f16_16816(sa[nb], a, q[2], q[3]);
+              }
+            }
+          }
+          // ---- scales: 2^ek on the score, ev in the weight's exponent
+          const float fa = e8m0_value(lds_u8(sc + key_a * Hkv));
+          const float fb = e8m0_value(lds_u8(sc + key_b * Hkv));
+          const int ca = lds_u8(sc + scale_bytes + key_a * Hkv);
+          const int cb_ = lds_u8(sc + scale_bytes + key_b * Hkv);
+          const float ea = ca == 255 ? __uint_as_float(0x7fc00000u) : (float)(ca - kE8m0Bias);
+          const float eb = cb_ == 255 ? __uint_as_float(0x7fc00000u) : (float)(cb_ - kE8m0Bias);
+          const bool edge = key_base < all_lo || key_base + kKB - 1 > all_hi;  // warp-uniform
+          uint32_t pw[NB][2 * kSplit];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            float s0 = sa[nb][0] * cs0[nb] * fa, s1 = sa[nb][1] * cs1[nb] * fa;
+            float s2 = sa[nb][2] * cs0[nb] * fb, s3 = sa[nb][3] * cs1[nb] * fb;
+            float t0 = s0 + ea, t1 = s1 + ea, t2 = s2 + eb, t3 = s3 + eb;
+            if (edge) {  // both: a slot that is not attended may hold any scale
+              const int h0 = d.pos0 + ((8 * nb + 2 * tq) >> p.lg_group);
+              const int h1 = d.pos0 + ((8 * nb + 2 * tq + 1) >> p.lg_group);
+              const int l0 = first_key(h0, W), l1 = first_key(h1, W);
+              if (ka < l0 || ka > h0) s0 = t0 = -INFINITY;
+              if (ka < l1 || ka > h1) s1 = t1 = -INFINITY;
+              if (kb < l0 || kb > h0) s2 = t2 = -INFINITY;
+              if (kb < l1 || kb > h1) s3 = t3 = -INFINITY;
+            }
+            float x0 = fmaxf(s0, s2), x1 = fmaxf(s1, s3);
+            float y0 = fmaxf(t0, t2), y1 = fmaxf(t1, t3);
+            if (__any_sync(0xffffffffu, x0 > m[nb][0] + kRaise || x1 > m[nb][1] + kRaise ||
+                                            y0 > mw[nb][0] + kRaise || y1 > mw[nb][1] + kRaise)) {
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) {
+                x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+                x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+                y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, off));
+                y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, off));
+              }
+              x0 = fmaxf(x0, m[nb][0]);
+              x1 = fmaxf(x1, m[nb][1]);
+              y0 = fmaxf(y0, mw[nb][0]);
+              y1 = fmaxf(y1, mw[nb][1]);
+              l[nb][0] *= ex2_approx(m[nb][0] - x0);
+              l[nb][1] *= ex2_approx(m[nb][1] - x1);
+              const float a0 = ex2_approx(mw[nb][0] - y0), a1 = ex2_approx(mw[nb][1] - y1);
+              m[nb][0] = x0;
+              m[nb][1] = x1;
+              mw[nb][0] = y0;
+              mw[nb][1] = y1;
+#pragma unroll
+              for (int e = 0; e < kKS; ++e) {
+                o[nb][e][0] *= a0;
+                o[nb][e][1] *= a1;
+                o[nb][e][2] *= a0;
+                o[nb][e][3] *= a1;
+              }
+            }
+            l[nb][0] += ex2_approx(s0 - m[nb][0]) + ex2_approx(s2 - m[nb][0]);
+            l[nb][1] += ex2_approx(s1 - m[nb][1]) + ex2_approx(s3 - m[nb][1]);
+            const float w0 = ex2_approx(t0 - mw[nb][0] + kWeightLog2);
+            const float w1 = ex2_approx(t1 - mw[nb][1] + kWeightLog2);
+            const float w2 = ex2_approx(t2 - mw[nb][0] + kWeightLog2);
+            const float w3 = ex2_approx(t3 - mw[nb][1] + kWeightLog2);
+            const uint32_t pa = pack_f16x2(w0, w1), pb = pack_f16x2(w2, w3);
+            pw[nb][0] = movmatrix_trans(pa);
+            pw[nb][1] = movmatrix_trans(pb);
+            if constexpr (F32) {
+              pw[nb][2] = movmatrix_trans(pack_f16x2_rest(pa, w0, w1));
+              pw[nb][3] = movmatrix_trans(pack_f16x2_rest(pb, w2, w3));
+            }
+          }
+          // ---- O^T += V^T P^T
+          uint32_t v[4][D / 32];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            if constexpr (D == 128) {
+              const uint4 x = lds128(st + v_off[r]);
+              v[r][0] = x.x;
+              v[r][1] = x.y;
+              v[r][2] = x.z;
+              v[r][3] = x.w;
+            } else {
+              const uint2 x = lds64(st + v_off[r]);
+              v[r][0] = x.x;
+              v[r][1] = x.y;
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.empty[s]);
+          if (key_base < any_lo || key_base + kKB - 1 > any_hi) {
+            // slots no row of the item attends hold anything, NaN codes too: weight 0 x value 0
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int key = key_base + v_key[r];
+              if (key < any_lo || key > any_hi)
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) v[r][e] = 0u;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) {
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+              const uint32_t sel = hi ? 0x7362u : 0x5140u;  // bytes of two keys side by side
+              const uint32_t x = __byte_perm(v[0][e], v[1][e], sel);
+              const uint32_t y = __byte_perm(v[2][e], v[3][e], sel);
+              const uint32_t a[4] = {f16x2_lo(x), f16x2_hi(x), f16x2_lo(y), f16x2_hi(y)};
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                mma_f16_16816(o[nb][2 * e + hi], a, pw[nb][0], pw[nb][1]);
+                if constexpr (F32) mma_f16_16816(o[nb][2 * e + hi], a, pw[nb][2], pw[nb][3]);
+              }
+            }
+          }
+        }
+        i0 += d.n;
+
+        // ---- the end of the piece: sums over the key rows of the columns
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1)
+              l[nb][c] += __shfl_xor_sync(0xffffffffu, l[nb][c], off);
+        // ---- join the KW warps of the head: warp 0 takes the others' states in rounds
+        if (KW > 1) {
+          constexpr int kRounds = NB * kKS * 4 / kXRegs;
+          float* of = &o[0][0][0];
+          if (kw > 0) {
+            const int xs = (kw - 1) * HB + hl;
+            float* x = xchg + xs * kXFloats + lane;
+#pragma unroll
+            for (int rd = 0; rd < kRounds; ++rd) {
+              const int ph = xphase + rd;
+              if (ph > 0 && !mbar_wait_warp_or_abort(&sm.xempty[xs], (uint32_t)(ph - 1) & 1, &sm.abort_flag)) {
+                give_up();
+                return;
+              }
+              if (rd == 0) {
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    x[(6 * nb + 3 * c) * 32] = m[nb][c];
+                    x[(6 * nb + 3 * c + 1) * 32] = mw[nb][c];
+                    x[(6 * nb + 3 * c + 2) * 32] = l[nb][c];
+                  }
+              }
+#pragma unroll
+              for (int e = 0; e < kXRegs; ++e) x[(6 * NB + e) * 32] = of[rd * kXRegs + e];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.xfull[xs]);
+            }
+          } else {
+            for (int w = 1; w < KW; ++w) {
+              const int xs = (w - 1) * HB + hl;
+              const float* x = xchg + xs * kXFloats + lane;
+              float own[NB][2], other[NB][2];
+#pragma unroll
+              for (int rd = 0; rd < kRounds; ++rd) {
+                const int ph = xphase + rd;
+                if (!mbar_wait_warp_or_abort(&sm.xfull[xs], (uint32_t)ph & 1, &sm.abort_flag)) {
+                  give_up();
+                  return;
+                }
+                if (rd == 0) {
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                      const float mo = x[(6 * nb + 3 * c) * 32], wo = x[(6 * nb + 3 * c + 1) * 32];
+                      const float mn = fmaxf(m[nb][c], mo), wn = fmaxf(mw[nb][c], wo);
+                      l[nb][c] = l[nb][c] * ex2_approx(m[nb][c] - mn) +
+                                 x[(6 * nb + 3 * c + 2) * 32] * ex2_approx(mo - mn);
+                      own[nb][c] = ex2_approx(mw[nb][c] - wn);
+                      other[nb][c] = ex2_approx(wo - wn);
+                      m[nb][c] = mn;
+                      mw[nb][c] = wn;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < kXRegs; ++e) {
+                  const int at = rd * kXRegs + e, nb = at / (kKS * 4), c = at & 1;
+                  of[at] = of[at] * own[nb][c] + x[(6 * NB + e) * 32] * other[nb][c];
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.xempty[xs]);
+              }
+            }
+          }
+          xphase += kRounds;
+          if (kw > 0) continue;
+        }
+        // ---- write: column 8 nb + 2 tq + c, outputs d = D/8 gid .. + D/8 - 1 of this lane
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int col = 8 * nb + 2 * tq + c;
+            const int tok = col >> p.lg_group;
+            if (tok >= d.ntok) continue;
+            const int h = head * G + (col & (G - 1));
+            // weights were relative to 2^(mw - kWeightLog2), the sum to 2^m
+            float f = ex2_approx(mw[nb][c] - kWeightLog2 - m[nb][c]);
+            if (d.direct) {
+              f = l[nb][c] != 0.f ? f / l[nb][c] : 0.f;
+              const long long at = ((long long)(d.t0 + tok) * Hq + h) * D + gid * (D / 8);
+              if constexpr (F32) {
+                float4* out = reinterpret_cast<float4*>(static_cast<float*>(p.a.out) + at);
+#pragma unroll
+                for (int e = 0; e < kKS; e += 2)
+                  out[e / 2] = make_float4(o[nb][e][c] * f, o[nb][e][2 + c] * f, o[nb][e + 1][c] * f,
+                                           o[nb][e + 1][2 + c] * f);
+              } else {
+                uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + at);
+#pragma unroll
+                for (int e = 0; e < kKS; e += 4) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int z = 0; z < 4; ++z)
+                    w[z] = pack_bf16x2(o[nb][e + z][c] * f, o[nb][e + z][2 + c] * f);
+                  out[e / 4] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+            } else {
+              const long long row = ((long long)d.slot * TT + tok) * Hq + h;
+              float4* out = reinterpret_cast<float4*>(p.part_o + row * D + gid * (D / 8));
+#pragma unroll
+              for (int e = 0; e < kKS; e += 2)
+                out[e / 2] = make_float4(o[nb][e][c] * f, o[nb][e][2 + c] * f, o[nb][e + 1][c] * f,
+                                         o[nb][e + 1][2 + c] * f);
+              if (gid == 0) p.part_ml[row] = make_float2(m[nb][c], l[nb][c]);
+            }
+          }
+        }
+      }
+    };
+    consume();
+  }
+  // As in the bf16 decode kernel: after a wait that gave up, the latest copy of each stage may
+  // be in flight; it is waited for before the shared memory is released.
+  __syncthreads();
+  if (warp == nwarps && lane == 0 && *reinterpret_cast<volatile int*>(&sm.abort_flag)) {
+    const int first = issued_blocks > p.stages ? issued_blocks - p.stages : 0;
+    for (int j = first; j < issued_blocks; ++j)
+      mbar_wait(&sm.full[j % p.stages], (uint32_t)(j / p.stages) & 1);
+  }
+}
+
+// ------------------------------------------------------------------ portable kernel
+//
+// One warp per (query row, KV head): walks the row's positions in order with a running
+// (max, sum, output) in fp32, as the portable kernel of the bf16/fp32 cache. For block sizes
+// below 16 (a key block of the split kernel must lie in one page).
+
+template <typename T, int VPT, int G>
+__global__ void __launch_bounds__(128) q8_portable_kernel(StepArgs a, Q8Cache c) {
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int lane = threadIdx.x & 31;
+  const int64_t idx = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int Hkv = a.num_kv_heads;
+  if (idx >= (int64_t)a.num_tokens * Hkv) return;
+  const int t = (int)(idx / Hkv);
+  const int g = (int)(idx % Hkv);
+  int lo_r = 0, hi_r = a.num_requests;
+  while (hi_r - lo_r > 1) {
+    const int mid = (lo_r + hi_r) >> 1;
+    if (__ldg(a.query_start_loc + mid) <= t) lo_r = mid; else hi_r = mid;
+  }
+  const int r = lo_r;
+  const int q_start = __ldg(a.query_start_loc + r);
+  const int q_len = __ldg(a.query_start_loc + r + 1) - q_start;
+  const int last = __ldg(a.seq_lens + r) - q_len + (t - q_start);
+  const int first = first_key(last, a.sliding_window);
+  constexpr int D = VPT * 32;
+  const T* q = static_cast<const T*>(a.q) + ((int64_t)t * a.num_q_heads + g * G) * D + lane * VPT;
+  float qv[G][VPT], m[G], l[G], o[G][VPT];
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    m[h] = -FLT_MAX;
+    l[h] = 0.f;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      qv[h][v] = Elt<T>::to_f(q[h * D + v]);
+      o[h][v] = 0.f;
+    }
+  }
+  const int32_t* bt = a.block_table + (int64_t)r * a.bt_stride;
+  for (int p = first; p <= last; ++p) {
+    const int blk = __ldg(bt + bt_entry(p / a.block_size, a.ring_blocks));
+    const bool ok = blk >= 0 && blk < a.num_blocks;
+    if (!ok && lane == 0) record_error(a.error_word, CB_DEVERR_BLOCK_ID);
+    const int64_t row = ok ? ((int64_t)blk * a.block_size + p % a.block_size) * Hkv + g : 0;
+    float kv[VPT], vv[VPT];
+    const float sk = ok ? e8m0_value(__ldg(c.k_scale + row)) : 0.f;
+    const float sv = ok ? e8m0_value(__ldg(c.v_scale + row)) : 0.f;
+#pragma unroll
+    for (int v = 0; v < VPT; v += 2) {
+      const uint16_t kk = ok ? *reinterpret_cast<const uint16_t*>(c.k + row * D + lane * VPT + v) : 0;
+      const uint16_t xx = ok ? *reinterpret_cast<const uint16_t*>(c.v + row * D + lane * VPT + v) : 0;
+      const float2 fk = float2_of_f16x2(f16x2_of_e4m3x2(kk)), fv = float2_of_f16x2(f16x2_of_e4m3x2(xx));
+      kv[v] = fk.x * sk;
+      kv[v + 1] = fk.y * sk;
+      vv[v] = fv.x * sv;
+      vv[v + 1] = fv.y * sv;
+    }
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      float s = 0.f;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) s = fmaf(qv[h][v], kv[v], s);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      s *= a.scale_log2;
+      const float mn = fmaxf(m[h], s);
+      const float alpha = exp2f(m[h] - mn);
+      const float pe = exp2f(s - mn);
+      l[h] = l[h] * alpha + pe;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) o[h][v] = fmaf(o[h][v], alpha, pe * vv[v]);
+      m[h] = mn;
+    }
+  }
+  T* out = static_cast<T*>(a.out) + ((int64_t)t * a.num_q_heads + g * G) * D + lane * VPT;
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    const float inv = l[h] > 0.f ? 1.f / l[h] : (l[h] == l[h] ? 0.f : l[h]);  // a NaN stays one
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) out[h * D + v] = Elt<T>::from_f(o[h][v] * inv);
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      ptr = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+
+// A cache as (d, key in page, head, page) bytes; the box (D, 16, HB, 1) lands as rows
+// (head, key) of D bytes.
+cudaError_t cache_map(CUtensorMap* map, void* cache, const StepArgs& a, int hb) {
+  auto fn = encode_fn();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t D = (cuuint64_t)a.head_dim, H = (cuuint64_t)a.num_kv_heads;
+  cuuint64_t dims[4] = {D, (cuuint64_t)a.block_size, H, (cuuint64_t)a.num_blocks};
+  cuuint64_t strides[3] = {H * D, D, (cuuint64_t)a.block_size * H * D};
+  cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)kKB, (cuuint32_t)hb, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, cache, dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D, int NB, bool F32>
+cudaError_t launch_split_t(const Q8Args& p, cudaStream_t s) {
+  auto kern = q8_split_kernel<D, NB, F32>;
+  const size_t smem = q8_smem_bytes(D, p.heads_per_cta, p.key_warps, NB, p.stages, p.a.num_kv_heads);
+  if (smem > (size_t)kQ8SmemLimit) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8SmemLimit);
+  if (e != cudaSuccess) return e;
+  CUtensorMap mk, mv;
+  e = cache_map(&mk, p.c.k, p.a, p.heads_per_cta);
+  if (e == cudaSuccess) e = cache_map(&mv, p.c.v, p.a, p.heads_per_cta);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kDecodeQ8, kern, dim3(p.num_ctas, p.a.num_kv_heads / p.heads_per_cta),
+                    dim3(p.heads_per_cta * p.key_warps * 32 + 32), smem, s, mk, mv, p);
+}
+
+template <int D>
+cudaError_t launch_split_d(const Q8Args& p, int nb, cudaStream_t s) {
+  if (p.a.dtype == CB_F32) {
+    if (nb == 1) return launch_split_t<D, 1, true>(p, s);
+    if (nb == 2) return launch_split_t<D, 2, true>(p, s);
+  } else {
+    if (nb == 1) return launch_split_t<D, 1, false>(p, s);
+    if (nb == 2) return launch_split_t<D, 2, false>(p, s);
+    if (nb == 4) return launch_split_t<D, 4, false>(p, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+template <typename T, int VPT>
+cudaError_t launch_portable_t(const StepArgs& a, const Q8Cache& c, cudaStream_t s) {
+  const int64_t warps = (int64_t)a.num_tokens * a.num_kv_heads;
+  const dim3 grid((unsigned)((warps + 3) / 4)), block(128);
+  switch (a.num_q_heads / a.num_kv_heads) {
+    case 1: return launch_pdl(kPortableQ8, q8_portable_kernel<T, VPT, 1>, grid, block, 0, s, a, c);
+    case 2: return launch_pdl(kPortableQ8, q8_portable_kernel<T, VPT, 2>, grid, block, 0, s, a, c);
+    case 4: return launch_pdl(kPortableQ8, q8_portable_kernel<T, VPT, 4>, grid, block, 0, s, a, c);
+    case 8: return launch_pdl(kPortableQ8, q8_portable_kernel<T, VPT, 8>, grid, block, 0, s, a, c);
+    case 16: return launch_pdl(kPortableQ8, q8_portable_kernel<T, VPT, 16>, grid, block, 0, s, a, c);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t q8_smem_bytes(int D, int HB, int KW, int NB, int stages, int Hkv) {
+  return 1024 /* alignment slack */ + (size_t)stages * (2 * HB * kKB * D + 2 * kKB * Hkv) +
+         (size_t)(KW - 1) * HB * (6 * NB + 16) * 128 /* exchange slots */ + sizeof(Q8Smem);
+}
+
+cudaError_t launch_q8_split(const Q8Args& p, int column_blocks, cudaStream_t stream) {
+  if (p.a.head_dim == 64) return launch_split_d<64>(p, column_blocks, stream);
+  return launch_split_d<128>(p, column_blocks, stream);
+}
+
+cudaError_t launch_q8_portable(const StepArgs& a, const Q8Cache& c, cudaStream_t stream) {
+  if (a.num_tokens <= 0) return cudaSuccess;
+  if (a.head_dim == 64)
+    return a.dtype == CB_F32 ? launch_portable_t<float, 2>(a, c, stream)
+                             : launch_portable_t<__nv_bfloat16, 2>(a, c, stream);
+  return a.dtype == CB_F32 ? launch_portable_t<float, 4>(a, c, stream)
+                           : launch_portable_t<__nv_bfloat16, 4>(a, c, stream);
+}
+
+}  // namespace cb

@@ -11,6 +11,7 @@
 #include <string>
 #include <unordered_map>
 
+#include "api.h"
 #include "cb.h"
 #include "launch.h"
 #include "plan.h"
@@ -72,6 +73,46 @@ namespace cb {
 // Status reporting for entry points defined in other files of the library.
 cb_status report_error(cb_status s, const char* msg) { return fail(s, msg); }
 cb_status report_cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+
+cb_status check_step_sizes(int32_t num_requests, int32_t num_tokens, int32_t num_blocks,
+                           int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                           int32_t head_dim, int32_t block_table_stride, int32_t dtype,
+                           const int32_t* h_query_start_loc, const int32_t* h_seq_lens) {
+  int elt = 0;
+  const cb_status st = check_dtype(dtype, &elt);
+  if (st != CB_OK) return st;
+  if (num_requests < 0 || num_tokens < 0)
+    return fail(CB_ERR_INVALID_ARG, "num_requests and num_tokens must be >= 0");
+  if (num_blocks <= 0 || block_size <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
+      head_dim <= 0 || block_table_stride < 0)
+    return fail(CB_ERR_INVALID_ARG, "sizes must be positive");
+  if (head_dim != 64 && head_dim != 128) return fail(CB_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (num_q_heads % num_kv_heads != 0)
+    return fail(CB_ERR_INVALID_ARG, "num_q_heads must be a multiple of num_kv_heads");
+  const int G = num_q_heads / num_kv_heads;
+  if (G != 1 && G != 2 && G != 4 && G != 8 && G != 16)
+    return fail(CB_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads must be 1, 2, 4, 8 or 16");
+  if (!is_pow2(block_size) || block_size > 256)
+    return fail(CB_ERR_UNSUPPORTED, "block_size must be a power of two <= 256");
+  if (!h_query_start_loc || !h_seq_lens)
+    return fail(CB_ERR_INVALID_ARG, "host mirrors of query_start_loc and seq_lens are required");
+  return CB_OK;
+}
+
+cb_status check_step_mirrors(const int32_t* h_query_start_loc, const int32_t* h_seq_lens,
+                             int32_t num_requests, int32_t block_size, int64_t* max_pages) {
+  if (h_query_start_loc[0] != 0) return fail(CB_ERR_METADATA, "query_start_loc[0] must be 0");
+  *max_pages = 0;
+  for (int r = 0; r < num_requests; ++r) {
+    const int32_t q_len = h_query_start_loc[r + 1] - h_query_start_loc[r];
+    if (q_len < 0) return fail(CB_ERR_METADATA, "query_start_loc must be non-decreasing");
+    if (q_len > h_seq_lens[r])
+      return fail(CB_ERR_METADATA, "seq_lens[r] must be >= q_len of request r");
+    const int64_t pages = ((int64_t)h_seq_lens[r] + block_size - 1) / block_size;
+    if (pages > *max_pages) *max_pages = pages;
+  }
+  return CB_OK;
+}
 
 }  // namespace cb
 
@@ -190,40 +231,20 @@ cb_status paged_attention_impl(cb_graph_cache* graph, void* out, const void* q, 
                                int32_t sliding_window, int32_t dtype, uint32_t flags,
                                void* workspace, size_t workspace_bytes, void* stream) {
   // ---- arguments
-  int elt = 0;
-  cb_status st = check_dtype(dtype, &elt);
+  cb_status st = cb::check_step_sizes(num_requests, num_tokens, num_blocks, block_size, num_q_heads,
+                                      num_kv_heads, head_dim, block_table_stride, dtype,
+                                      h_query_start_loc, h_seq_lens);
   if (st != CB_OK) return st;
-  if (num_requests < 0 || num_tokens < 0)
-    return fail(CB_ERR_INVALID_ARG, "num_requests and num_tokens must be >= 0");
-  if (num_blocks <= 0 || block_size <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 ||
-      head_dim <= 0 || block_table_stride < 0)
-    return fail(CB_ERR_INVALID_ARG, "sizes must be positive");
-  if (head_dim != 64 && head_dim != 128) return fail(CB_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
-  if (num_q_heads % num_kv_heads != 0)
-    return fail(CB_ERR_INVALID_ARG, "num_q_heads must be a multiple of num_kv_heads");
-  const int G = num_q_heads / num_kv_heads;
-  if (G != 1 && G != 2 && G != 4 && G != 8 && G != 16)
-    return fail(CB_ERR_UNSUPPORTED, "num_q_heads / num_kv_heads must be 1, 2, 4, 8 or 16");
-  if (!is_pow2(block_size) || block_size > 256)
-    return fail(CB_ERR_UNSUPPORTED, "block_size must be a power of two <= 256");
-  if (!h_query_start_loc || !h_seq_lens)
-    return fail(CB_ERR_INVALID_ARG, "host mirrors of query_start_loc and seq_lens are required");
+  const int elt = dtype == CB_F32 ? 4 : 2;
   if (!workspace || workspace_bytes < cb::workspace_bytes(num_requests, num_tokens, num_q_heads,
                                                           num_kv_heads, head_dim))
     return fail(CB_ERR_WORKSPACE, "workspace missing or smaller than cb_workspace_size()");
   if (!aligned16(workspace)) return fail(CB_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
 
   // ---- host mirrors of the metadata
-  if (h_query_start_loc[0] != 0) return fail(CB_ERR_METADATA, "query_start_loc[0] must be 0");
   int64_t max_pages = 0;
-  for (int r = 0; r < num_requests; ++r) {
-    const int32_t q_len = h_query_start_loc[r + 1] - h_query_start_loc[r];
-    if (q_len < 0) return fail(CB_ERR_METADATA, "query_start_loc must be non-decreasing");
-    if (q_len > h_seq_lens[r])
-      return fail(CB_ERR_METADATA, "seq_lens[r] must be >= q_len of request r");
-    const int64_t pages = ((int64_t)h_seq_lens[r] + block_size - 1) / block_size;
-    if (pages > max_pages) max_pages = pages;
-  }
+  st = cb::check_step_mirrors(h_query_start_loc, h_seq_lens, num_requests, block_size, &max_pages);
+  if (st != CB_OK) return st;
   if (graph) {
     // padded shape: num_requests and num_tokens multiples of the query interval;
     // the tokens past query_start_loc[R] (and requests with q_len 0) are padding

@@ -1,0 +1,274 @@
+// Quantising writes into the 8-bit paged cache and reads back from it.
+//
+// write_kv_q8: the step's new K/V rows go to the cache slots that slot_mapping names, as
+// write_kv does ("Continuous Batching", languisher.top, section "Extension: the vLLM v1
+// implementation": the scheduler builds slot_mapping), rounded to e4m3 with one scale per
+// row on the way (q8.cuh). read_kv_q8: the rows at given slots, back in the caller's type.
+// dequant_pages_q8: the pages of whole requests as bf16 pages, for the prefill tiles.
+//
+// All three are one pass over the data, HBM-bound: 16 values per thread, the D / 16 threads
+// of a row side by side in a warp, so that the row's largest magnitude is a shuffle over 8
+// (D 128) or 4 (D 64) lanes and every access is a full 16- or 32-byte vector. A thread takes
+// the K row and the V row of its token and head: two independent loads in flight, one slot
+// lookup.
+#include "common.cuh"
+#include "launch.h"
+#include "q8.cuh"
+#include "q8.h"
+
+namespace cb {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVals = 16;  // values of a row per thread
+
+CB_DEV void load16(const float* p, float (&x)[kVals]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(p) + i);
+    x[4 * i] = v.x;
+    x[4 * i + 1] = v.y;
+    x[4 * i + 2] = v.z;
+    x[4 * i + 3] = v.w;
+  }
+}
+
+CB_DEV void load16(const __nv_bfloat16* p, float (&x)[kVals]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+      x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+}
+
+CB_DEV void store16(float* p, const float (&x)[kVals]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+}
+
+CB_DEV void store16(__nv_bfloat16* p, const float (&x)[kVals]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[8 * i + 2 * j], x[8 * i + 2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    reinterpret_cast<uint4*>(p)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// 16 e4m3 values times the row's scale.
+CB_DEV void dequant16(uint4 v, float scale, float (&x)[kVals]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = float2_of_f16x2(f16x2_of_e4m3x2((uint16_t)w[i]));
+    const float2 b = float2_of_f16x2(f16x2_of_e4m3x2((uint16_t)(w[i] >> 16)));
+    x[4 * i] = a.x * scale;
+    x[4 * i + 1] = a.y * scale;
+    x[4 * i + 2] = b.x * scale;
+    x[4 * i + 3] = b.y * scale;
+  }
+}
+
+// Quantise the 16 values of this thread and store them; the row's threads (LPR lanes, all of
+// them here) agree on its scale, which the first of them stores.
+template <int LPR>
+CB_DEV void quant_store(const float (&x)[kVals], uint8_t* row, uint8_t* code_at, int part) {
+  uint32_t a = 0u;
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) a = max(a, finite_magnitude(x[i]));
+#pragma unroll
+  for (int off = LPR / 2; off > 0; off >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
+  const int code = e8m0_of_magnitude(a);
+  const float inv = e8m0_inverse(code);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = e4m3x2_of(x[4 * i] * inv, x[4 * i + 1] * inv) |
+           (e4m3x2_of(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
+  if (row != nullptr) {
+    reinterpret_cast<uint4*>(row)[part] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (part == 0) *code_at = (uint8_t)code;
+  }
+}
+
+}  // namespace
+
+// Thread i: values 16 (i % LPR) .. + 15 of the K and the V row i / LPR = (token, head).
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+write_kv_q8_kernel(const T* __restrict__ k_new, const T* __restrict__ v_new, Q8Cache c,
+                   const int64_t* __restrict__ slot_mapping, int64_t rows, int32_t Hkv,
+                   int64_t num_slots, int32_t* error_word) {
+  constexpr int LPR = D / kVals;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t row = i / LPR;
+  const int part = (int)(i % LPR);
+  const bool live = row < rows;
+  float xk[kVals] = {}, xv[kVals] = {};
+  int64_t dst = -1;  // row index in the cache
+  if (live) {
+    const int64_t t = row / Hkv;
+    const int64_t slot = __ldg(slot_mapping + t);
+    load16(k_new + row * D + part * kVals, xk);
+    load16(v_new + row * D + part * kVals, xv);
+    if (slot >= num_slots) {
+      if (part == 0) record_error(error_word, 0x2);
+    } else if (slot >= 0) {
+      dst = slot * Hkv + (row - t * Hkv);
+    }
+  }
+  // every lane takes part in the shuffles; a row without a slot is not stored
+  quant_store<LPR>(xk, dst >= 0 ? c.k + dst * D : nullptr, c.k_scale + dst, part);
+  quant_store<LPR>(xv, dst >= 0 ? c.v + dst * D : nullptr, c.v_scale + dst, part);
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+read_kv_q8_kernel(T* __restrict__ k_out, T* __restrict__ v_out, Q8Cache c,
+                  const int64_t* __restrict__ slot_mapping, int64_t rows, int32_t Hkv,
+                  int64_t num_slots, int32_t* error_word) {
+  constexpr int LPR = D / kVals;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t row = i / LPR;
+  const int part = (int)(i % LPR);
+  if (row >= rows) return;
+  const int64_t t = row / Hkv;
+  const int64_t slot = __ldg(slot_mapping + t);
+  if (slot < 0) return;
+  if (slot >= num_slots) {
+    if (part == 0) record_error(error_word, 0x2);
+    return;
+  }
+  const int64_t src = slot * Hkv + (row - t * Hkv);
+  const uint4 k = __ldg(reinterpret_cast<const uint4*>(c.k + src * D) + part);
+  const uint4 v = __ldg(reinterpret_cast<const uint4*>(c.v + src * D) + part);
+  const float sk = e8m0_value(__ldg(c.k_scale + src));
+  const float sv = e8m0_value(__ldg(c.v_scale + src));
+  float x[kVals];
+  dequant16(k, sk, x);
+  store16(k_out + row * D + part * kVals, x);
+  dequant16(v, sv, x);
+  store16(v_out + row * D + part * kVals, x);
+}
+
+// One CTA per destination page. A page id out of range reads as zeros.
+template <int D>
+__global__ void __launch_bounds__(kThreads) dequant_pages_q8_kernel(const __grid_constant__ DequantArgs d) {
+  constexpr int LPR = D / kVals;
+  grid_dependency_wait();
+  allow_dependent_launch();
+  const int page = d.dst0 + blockIdx.x;
+  int lo = 0, hi = d.n_entries;  // entries[lo].dst <= page < entries[hi].dst
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (d.entries[mid].dst <= page) lo = mid; else hi = mid;
+  }
+  const DequantEntry& e = d.entries[lo];
+  const int lp = e.first + (page - e.dst);
+  const int src = __ldg(d.block_table + (int64_t)e.r * d.bt_stride + lp);
+  const bool ok = src >= 0 && src < d.num_blocks;
+  if (threadIdx.x == 0) {
+    d.table[e.row + lp] = page;
+    if (!ok) record_error(d.error_word, 0x1);
+  }
+  const int rows = d.block_size * d.num_kv_heads;
+  const int64_t from = (int64_t)(ok ? src : 0) * rows, to = (int64_t)page * rows;
+  __nv_bfloat16* ko = static_cast<__nv_bfloat16*>(d.k) + to * D;
+  __nv_bfloat16* vo = static_cast<__nv_bfloat16*>(d.v) + to * D;
+  for (int i = threadIdx.x; i < rows * LPR; i += kThreads) {
+    const int row = i / LPR;
+    uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
+    float sk = 0.f, sv = 0.f;
+    if (ok) {
+      k = __ldg(reinterpret_cast<const uint4*>(d.c.k + from * D) + i);
+      v = __ldg(reinterpret_cast<const uint4*>(d.c.v + from * D) + i);
+      sk = e8m0_value(__ldg(d.c.k_scale + from + row));
+      sv = e8m0_value(__ldg(d.c.v_scale + from + row));
+    }
+    float x[kVals];
+    dequant16(k, sk, x);
+    store16(ko + i * kVals, x);
+    dequant16(v, sv, x);
+    store16(vo + i * kVals, x);
+  }
+}
+
+namespace {
+
+template <typename T>
+cudaError_t launch_write_t(const T* k, const T* v, const Q8Cache& c, const int64_t* slots,
+                           int64_t rows, int32_t Hkv, int32_t D, int64_t num_slots, int32_t* err,
+                           cudaStream_t s) {
+  const dim3 grid((unsigned)((rows * (D / kVals) + kThreads - 1) / kThreads));
+  if (D == 64)
+    return launch_pdl(kWriteKvQ8, write_kv_q8_kernel<T, 64>, grid, dim3(kThreads), 0, s, k, v, c,
+                      slots, rows, Hkv, num_slots, err);
+  return launch_pdl(kWriteKvQ8, write_kv_q8_kernel<T, 128>, grid, dim3(kThreads), 0, s, k, v, c,
+                    slots, rows, Hkv, num_slots, err);
+}
+
+template <typename T>
+cudaError_t launch_read_t(T* k, T* v, const Q8Cache& c, const int64_t* slots, int64_t rows,
+                          int32_t Hkv, int32_t D, int64_t num_slots, int32_t* err,
+                          cudaStream_t s) {
+  const dim3 grid((unsigned)((rows * (D / kVals) + kThreads - 1) / kThreads));
+  if (D == 64)
+    return launch_pdl(kReadKvQ8, read_kv_q8_kernel<T, 64>, grid, dim3(kThreads), 0, s, k, v, c,
+                      slots, rows, Hkv, num_slots, err);
+  return launch_pdl(kReadKvQ8, read_kv_q8_kernel<T, 128>, grid, dim3(kThreads), 0, s, k, v, c,
+                    slots, rows, Hkv, num_slots, err);
+}
+
+}  // namespace
+
+cudaError_t launch_write_kv_q8(const void* k_new, const void* v_new, const Q8Cache& c,
+                               const int64_t* slot_mapping, int32_t num_tokens, int64_t num_slots,
+                               int32_t Hkv, int32_t D, int32_t dtype, int32_t* error_word,
+                               cudaStream_t s) {
+  if (num_tokens <= 0) return cudaSuccess;
+  const int64_t rows = (int64_t)num_tokens * Hkv;
+  if (dtype == 0)
+    return launch_write_t(static_cast<const float*>(k_new), static_cast<const float*>(v_new), c,
+                          slot_mapping, rows, Hkv, D, num_slots, error_word, s);
+  return launch_write_t(static_cast<const __nv_bfloat16*>(k_new),
+                        static_cast<const __nv_bfloat16*>(v_new), c, slot_mapping, rows, Hkv, D,
+                        num_slots, error_word, s);
+}
+
+cudaError_t launch_read_kv_q8(void* k_out, void* v_out, const Q8Cache& c,
+                              const int64_t* slot_mapping, int32_t num_tokens, int64_t num_slots,
+                              int32_t Hkv, int32_t D, int32_t dtype, int32_t* error_word,
+                              cudaStream_t s) {
+  if (num_tokens <= 0) return cudaSuccess;
+  const int64_t rows = (int64_t)num_tokens * Hkv;
+  if (dtype == 0)
+    return launch_read_t(static_cast<float*>(k_out), static_cast<float*>(v_out), c, slot_mapping,
+                         rows, Hkv, D, num_slots, error_word, s);
+  return launch_read_t(static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), c,
+                       slot_mapping, rows, Hkv, D, num_slots, error_word, s);
+}
+
+cudaError_t launch_dequant_pages_q8(const DequantArgs& d, cudaStream_t s) {
+  if (d.n_pages <= 0) return cudaSuccess;
+  const dim3 grid((unsigned)d.n_pages);
+  if (d.head_dim == 64)
+    return launch_pdl(kDequantPages, dequant_pages_q8_kernel<64>, grid, dim3(kThreads), 0, s, d);
+  return launch_pdl(kDequantPages, dequant_pages_q8_kernel<128>, grid, dim3(kThreads), 0, s, d);
+}
+
+}  // namespace cb

@@ -36,7 +36,13 @@ enum KernelId {
   kPrefillTc = 3,
   kCopyBlocks = 4,
   kDecodeCombine = 5,
-  kNumKernels = 6
+  kWriteKvQ8 = 6,
+  kReadKvQ8 = 7,
+  kDecodeQ8 = 8,
+  kPortableQ8 = 9,
+  kMergeRowsId = 10,
+  kDequantPages = 11,
+  kNumKernels = 12
 };
 
 void note_launch_begin(KernelId id, cudaStream_t stream);

@@ -1,0 +1,118 @@
+// out = sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s over the pieces s of a row, M = max_s m_s:
+// the log-sum-exp join of partial softmax results (m_s the piece's running maximum in log2
+// units, l_s its sum, o_s its unnormalised output). The statistics stay in fp32.
+//
+// Latency-bound: the pieces were just written and lie in L2, so what counts is the number of
+// dependent rounds of loads. A thread takes four consecutive outputs and has the loads of up
+// to eight pieces in flight; a row of many pieces is shared by `parts` threads per output,
+// which join through shared memory.
+#include <float.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "merge.h"
+
+namespace cb {
+
+namespace {
+
+constexpr int kInFlight = 8;
+
+struct Acc {
+  float m, l;
+  float4 o;
+};
+
+CB_DEV void join(Acc& x, float m, float l, float4 o) {
+  const float M = fmaxf(x.m, m);
+  const float a = exp2f(x.m - M), b = exp2f(m - M);
+  x.m = M;
+  x.l = x.l * a + l * b;
+  x.o.x = x.o.x * a + o.x * b;
+  x.o.y = x.o.y * a + o.y * b;
+  x.o.z = x.o.z * a + o.z * b;
+  x.o.w = x.o.w * a + o.w * b;
+}
+
+}  // namespace
+
+template <typename T>
+__global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(const MergeArgs m) {
+  __shared__ float4 sh_o[kMergeThreads];
+  __shared__ float2 sh_ml[kMergeThreads];
+  const MergeRow& row = m.rows[blockIdx.x];
+  const int per = kMergeThreads / m.parts;  // outputs (of four values) per CTA
+  const int part = threadIdx.x / per;
+  const int f = blockIdx.y * per + threadIdx.x % per;
+  const int F = m.num_q_heads * m.head_dim / 4;
+  const int h = f * 4 / m.head_dim;
+  const int n = row.na + row.nb;
+  allow_dependent_launch();
+  grid_dependency_wait();
+  Acc x{-FLT_MAX, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (f < F) {
+    const float4* o = reinterpret_cast<const float4*>(m.part_o);
+    const int s1 = (part + 1) * n / m.parts;
+    for (int s0 = part * n / m.parts; s0 < s1; s0 += kInFlight) {
+      float2 ml[kInFlight];
+      float4 v[kInFlight];
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i) {
+        const int s = s0 + i;
+        if (s < s1) {
+          const long long pr = s < row.na ? (long long)row.a + (long long)s * row.a_step
+                                          : (long long)row.b + (long long)(s - row.na) * row.b_step;
+          ml[i] = __ldcg(m.part_ml + pr * m.num_q_heads + h);
+          v[i] = __ldcg(o + pr * F + f);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i)
+        if (s0 + i < s1) join(x, ml[i].x, ml[i].y, v[i]);
+    }
+  }
+  if (m.parts > 1) {
+    sh_o[threadIdx.x] = x.o;
+    sh_ml[threadIdx.x] = make_float2(x.m, x.l);
+    __syncthreads();
+    if (part == 0)
+      for (int q = 1; q < m.parts; ++q) {
+        const float2 ml = sh_ml[q * per + threadIdx.x];
+        join(x, ml.x, ml.y, sh_o[q * per + threadIdx.x]);
+      }
+  }
+  if (part != 0 || f >= F) return;
+  const float inv = x.l != 0.f ? 1.f / x.l : 0.f;
+  T* out = static_cast<T*>(m.out) + (long long)row.t * F * 4 + 4 * f;
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(out) = make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv);
+  } else {
+    __nv_bfloat162 a = __floats2bfloat162_rn(x.o.x * inv, x.o.y * inv);
+    __nv_bfloat162 b = __floats2bfloat162_rn(x.o.z * inv, x.o.w * inv);
+    *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+  }
+}
+
+int merge_parts(int pieces) {
+  int parts = 1;
+  while (parts < 8 && pieces > kInFlight * parts) parts *= 2;
+  return parts;
+}
+
+cudaError_t launch_merge(MergeArgs& m, const MergeRow* rows, int n, cudaStream_t stream) {
+  const int per = kMergeThreads / m.parts;
+  const int F = m.num_q_heads * m.head_dim / 4;
+  for (int i = 0; i < n; i += kMergeRows) {
+    m.n = std::min(kMergeRows, n - i);
+    std::copy(rows + i, rows + i + m.n, m.rows);
+    const dim3 grid(m.n, (F + per - 1) / per);
+    const cudaError_t e =
+        m.dtype == 0 ? launch_pdl(kMergeRowsId, merge_rows_kernel<float>, grid, dim3(kMergeThreads), 0, stream, m)
+                     : launch_pdl(kMergeRowsId, merge_rows_kernel<__nv_bfloat16>, grid, dim3(kMergeThreads), 0, stream, m);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace cb

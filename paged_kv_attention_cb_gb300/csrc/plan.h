@@ -18,6 +18,9 @@ constexpr size_t kScatterCounterOffset = 192;  // int: prefill row-copy parts cl
 constexpr int kMaxDecodeCtas = 2048;           // upper bound on decode CTAs (workspace sizing)
 constexpr int kMaxPrefillLaunches = 8;         // x kPrefillMaxEntries prefill requests per step
 
+// Multiprocessors of the current device.
+int sm_count();
+
 size_t workspace_bytes(int32_t num_requests, int32_t num_tokens, int32_t num_q_heads,
                        int32_t num_kv_heads, int32_t head_dim);
 

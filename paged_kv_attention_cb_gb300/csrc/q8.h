@@ -1,0 +1,96 @@
+// The 8-bit paged cache: launchers and arguments shared by its kernels and the planner.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "launch.h"
+#include "merge.h"
+
+namespace cb {
+
+// k, v: [num_blocks, block_size, Hkv, D] e4m3; k_scale, v_scale: [num_blocks, block_size, Hkv]
+// e8m0 (one power of two per row).
+struct Q8Cache {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+};
+
+cudaError_t launch_write_kv_q8(const void* k_new, const void* v_new, const Q8Cache& c,
+                               const int64_t* slot_mapping, int32_t num_tokens, int64_t num_slots,
+                               int32_t Hkv, int32_t D, int32_t dtype, int32_t* error_word,
+                               cudaStream_t stream);
+
+cudaError_t launch_read_kv_q8(void* k_out, void* v_out, const Q8Cache& c,
+                              const int64_t* slot_mapping, int32_t num_tokens, int64_t num_slots,
+                              int32_t Hkv, int32_t D, int32_t dtype, int32_t* error_word,
+                              cudaStream_t stream);
+
+// ---- split kernel (attn_q8.cu): rows of requests with 1 <= q_len <= max_q
+
+constexpr int kQ8KeyBlock = 16;      // keys per unit of work (and per stage of the ring)
+constexpr int kQ8MaxStages = 32;
+constexpr int kQ8MaxHeads = 8;       // KV heads per CTA
+constexpr int kQ8TableCtas = 192;    // CTAs per group of heads (their starts are arguments)
+constexpr int kQ8SmemLimit = 232448; // 227 KiB dynamic shared memory per CTA
+constexpr int kQ8MinBlocksPerCta = 4;
+
+// Where a CTA's range of key blocks starts.
+struct Q8CtaStart {
+  int r;     // request (-1: none)
+  int tile;  // token tile within the request
+  int u0;    // global index of that item's first key block
+};
+
+struct Q8Args {
+  StepArgs a;  // k_cache / v_cache unused
+  Q8Cache c;
+  int total_units;    // U: key blocks of all items
+  int num_ctas;       // C: CTA b takes blocks [b U / C, (b + 1) U / C)
+  int heads_per_cta;  // HB
+  int key_warps;      // KW: warps per KV head; block i goes to warp i % KW
+  int stages;         // multiple of KW
+  int tile_tokens;    // TT: query tokens per item (TT * G columns, at most 8 NB)
+  int lg_group;       // log2 of query heads per KV head
+  int max_q;
+  float* part_o;      // [slot * TT + token][Hq][D]: CTA b's first piece has slot 2 b, its last
+                      // 2 b + 1 (an item between them lies in the CTA and is written directly)
+  float2* part_ml;    // [slot * TT + token][Hq]
+  Q8CtaStart start[kQ8TableCtas];
+};
+
+// Column blocks (of 8 columns) a CTA's items have: 1, 2 or 4; fp32 queries at most 2.
+cudaError_t launch_q8_split(const Q8Args& p, int column_blocks, cudaStream_t stream);
+size_t q8_smem_bytes(int D, int HB, int KW, int NB, int stages, int Hkv);
+
+// One warp per (row, KV head) on the CUDA cores: every shape, no split.
+cudaError_t launch_q8_portable(const StepArgs& a, const Q8Cache& c, cudaStream_t stream);
+
+// ---- whole requests as bf16 pages (kv_q8.cu), for the prefill tiles
+
+constexpr int kDequantMaxEntries = 128;
+
+// Logical pages first .. first + n - 1 of request r become destination pages dst .. dst + n - 1,
+// and table[row + first + i] = dst + i.
+struct DequantEntry {
+  int r, first, n, dst, row;
+};
+
+struct DequantArgs {
+  Q8Cache c;
+  const int32_t* block_table;
+  int bt_stride;
+  int num_blocks, block_size, num_kv_heads, head_dim;
+  void *k, *v;     // [pages, block_size, Hkv, D] bf16
+  int32_t* table;  // logical page -> destination page, the requests' rows one after the other
+  int32_t* error_word;
+  int dst0, n_pages;  // destination pages dst0 .. dst0 + n_pages - 1, in the entries' order
+  int n_entries;
+  DequantEntry entries[kDequantMaxEntries];
+};
+
+cudaError_t launch_dequant_pages_q8(const DequantArgs& d, cudaStream_t stream);
+
+}  // namespace cb

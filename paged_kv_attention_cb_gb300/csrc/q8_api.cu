@@ -1,0 +1,434 @@
+// Entry points of the 8-bit paged cache (declared in include/cb.h): validation, planning from
+// the host mirrors and the launches of one step.
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <algorithm>
+#include <climits>
+#include <vector>
+
+#include "api.h"
+#include "cb.h"
+#include "launch.h"
+#include "merge.h"
+#include "plan.h"
+#include "q8.h"
+
+namespace {
+
+using cb::report_error;
+
+constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Requests of more query columns (tokens x grouped heads) than this are prefilled: their pages
+// are turned into bf16 once and the tcgen05 tiles read those. Below it the split kernel reads
+// the 8-bit pages directly, once per 32 columns.
+constexpr int kChunkColumns = 64;
+constexpr int kMaxColumns = 32;  // columns of a split kernel's item at most
+
+int heads_per_cta(int Hkv) {
+  int hb = std::min(Hkv, cb::kQ8MaxHeads);
+  while (Hkv % hb != 0) --hb;
+  return hb;
+}
+
+// Workspace: header (as cb_paged_attention's), statistics and outputs of the partial rows, then
+// the scratch of the prefilled requests (page table, K pages, V pages), whose sizes follow from
+// each step's lengths. The partial rows: two pieces per CTA of up to kMaxColumns / G tokens.
+struct Layout {
+  size_t part_ml, part_o, scratch;
+};
+
+Layout layout_of(int Hkv, int D) {
+  // rows x Hq = 2 C (kMaxColumns / G) Hkv G, with C head groups' worth of at most kQ8TableCtas
+  const size_t entries = (size_t)2 * cb::kQ8TableCtas * kMaxColumns * heads_per_cta(Hkv) *
+                         std::max(1, Hkv / heads_per_cta(Hkv) / cb::kQ8TableCtas + 1);
+  Layout w;
+  w.part_ml = cb::kWorkspaceHeaderBytes;
+  w.part_o = w.part_ml + align256(entries * 8);
+  w.scratch = w.part_o + align256(entries * D * 4);
+  return w;
+}
+
+size_t scratch_bytes(int64_t table_pages, int64_t pages, int block_size, int Hkv, int D) {
+  return align256((size_t)table_pages * 4) + 2 * (size_t)pages * block_size * Hkv * D * 2;
+}
+
+struct Q8Plan {
+  bool split = false;
+  int column_blocks = 1;
+  cb::Q8Args args;
+  std::vector<cb::MergeRow> merge;
+  int max_pieces = 0;
+  std::vector<cb::PrefillEntry> chunks;  // heaviest first
+};
+
+int first_key(int pos0, int window) { return window > 0 ? std::max(0, pos0 - window + 1) : 0; }
+
+// The split kernel's launch over the requests with 1 <= q_len <= max_q.
+void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int max_q,
+                const int32_t* qsl, const int32_t* seq_lens, uint8_t* ws) {
+  const int G = a.num_q_heads / a.num_kv_heads;
+  int longest = 0;
+  for (int r = 0; r < a.num_requests; ++r) {
+    const int q = qsl[r + 1] - qsl[r];
+    if (q <= max_q) longest = std::max(longest, q);
+  }
+  if (longest == 0) return;
+  plan.split = true;
+  const int top = a.dtype == CB_F32 ? 2 : 4;  // column blocks (fp32 queries: twice the operands)
+  int nb = 1;
+  while (nb < top && 8 * nb < std::min<int64_t>((int64_t)longest * G, kMaxColumns)) nb *= 2;
+  plan.column_blocks = nb;
+
+  cb::Q8Args& p = plan.args;
+  p.a = a;
+  p.c = c;
+  p.max_q = max_q;
+  p.tile_tokens = 8 * nb / G;
+  p.lg_group = 0;
+  while ((1 << p.lg_group) < G) ++p.lg_group;
+  const int HB = p.heads_per_cta = heads_per_cta(a.num_kv_heads);
+  // warps per head: as many as the register budget of the column blocks allows (16 consumer
+  // warps of 120 registers, or 8 of 224), so that few heads still fill the SM
+  p.key_warps = 1;
+  while (p.key_warps < 8 && 2 * p.key_warps * HB <= (nb == 1 ? 16 : 8)) p.key_warps *= 2;
+  const size_t fixed = cb::q8_smem_bytes(a.head_dim, HB, p.key_warps, nb, 0, a.num_kv_heads);
+  const size_t per = cb::q8_smem_bytes(a.head_dim, HB, p.key_warps, nb, 1, a.num_kv_heads) - fixed;
+  p.stages = (int)std::min<size_t>(cb::kQ8MaxStages, (cb::kQ8SmemLimit - fixed) / per);
+  p.stages -= p.stages % p.key_warps;
+
+  const int TT = p.tile_tokens, W = a.sliding_window;
+  auto blocks = [&](int pos0, int ntok) {
+    return (pos0 + ntok - 1) / cb::kQ8KeyBlock - first_key(pos0, W) / cb::kQ8KeyBlock + 1;
+  };
+  long long U = 0;
+  auto each_item = [&](auto&& f) {
+    for (int r = 0; r < a.num_requests; ++r) {
+      const int q = qsl[r + 1] - qsl[r];
+      if (q < 1 || q > max_q) continue;
+      for (int i = 0; i * TT < q; ++i) f(r, i, seq_lens[r] - q + i * TT, std::min(TT, q - i * TT));
+    }
+  };
+  each_item([&](int, int, int pos0, int ntok) { U += blocks(pos0, ntok); });
+  const int groups = a.num_kv_heads / HB;
+  long long C = std::max(1, std::min(cb::sm_count(), cb::kQ8TableCtas) / groups);
+  C = std::min(C, (U + cb::kQ8MinBlocksPerCta - 1) / cb::kQ8MinBlocksPerCta);
+  p.total_units = (int)U;
+  p.num_ctas = (int)C;
+
+  // where each CTA's range starts, and the items that several CTAs share
+  auto start_of = [&](long long b) { return b * U / C; };
+  long long u = 0;
+  int b = 0;
+  each_item([&](int r, int tile, int pos0, int ntok) {
+    const int n = blocks(pos0, ntok);
+    for (; b < C && start_of(b) < u + n; ++b) p.start[b] = cb::Q8CtaStart{r, tile, (int)u};
+    const int b0 = (int)(((u + 1) * C + U - 1) / U) - 1;
+    const int b1 = (int)(((u + n) * C + U - 1) / U) - 1;
+    if (b1 > b0) {
+      const int slot0 = 2 * b0 + (u > start_of(b0) ? 1 : 0);
+      for (int i = 0; i < ntok; ++i)
+        plan.merge.push_back(cb::MergeRow{qsl[r] + tile * TT + i, slot0 * TT + i, 0, 1,
+                                          2 * (b0 + 1) * TT + i, 2 * TT, b1 - b0});
+      plan.max_pieces = std::max(plan.max_pieces, b1 - b0 + 1);
+    }
+    u += n;
+  });
+  const Layout w = layout_of(a.num_kv_heads, a.head_dim);
+  p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
+  p.part_o = reinterpret_cast<float*>(ws + w.part_o);
+}
+
+// Bytes the prefilled requests need behind the partial rows; fills plan.chunks.
+size_t plan_chunks(Q8Plan& plan, const cb::StepArgs& a, int max_q, const int32_t* qsl,
+                   const int32_t* seq_lens) {
+  const int TQ = 128 / (a.num_q_heads / a.num_kv_heads);
+  int64_t pages = 0, table = 0;
+  for (int r = 0; r < a.num_requests; ++r) {
+    const int q = qsl[r + 1] - qsl[r];
+    if (q <= max_q) continue;
+    plan.chunks.push_back(cb::PrefillEntry{r, (q + TQ - 1) / TQ, qsl[r], q, seq_lens[r]});
+    const int64_t all = ((int64_t)seq_lens[r] + a.block_size - 1) / a.block_size;
+    table += all;
+    pages += all - first_key(seq_lens[r] - q, a.sliding_window) / 128 * 128 / a.block_size;
+  }
+  if (plan.chunks.empty()) return 0;
+  std::stable_sort(plan.chunks.begin(), plan.chunks.end(), [](const auto& x, const auto& y) {
+    return (long long)x.seq_len * x.q_len > (long long)y.seq_len * y.q_len;
+  });
+  return scratch_bytes(table, pages, a.block_size, a.num_kv_heads, a.head_dim);
+}
+
+// The prefilled requests, up to kPrefillMaxEntries a launch: their pages as bf16, then the tiles.
+cudaError_t run_chunks(const Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c,
+                       uint8_t* ws, cudaStream_t s) {
+  int64_t table = 0, total = 0;
+  for (const cb::PrefillEntry& e : plan.chunks) {
+    const int64_t all = ((int64_t)e.seq_len + a.block_size - 1) / a.block_size;
+    table += all;
+    total += all - first_key(e.seq_len - e.q_len, a.sliding_window) / 128 * 128 / a.block_size;
+  }
+  uint8_t* scratch = ws + layout_of(a.num_kv_heads, a.head_dim).scratch;
+  uint8_t* k = scratch + align256((size_t)table * 4);
+  uint8_t* v = k + (size_t)total * a.block_size * a.num_kv_heads * a.head_dim * 2;
+  int row = 0, dst = 0;
+  for (size_t i = 0; i < plan.chunks.size(); i += cb::kPrefillMaxEntries) {
+    const int n = (int)std::min<size_t>(cb::kPrefillMaxEntries, plan.chunks.size() - i);
+    cb::DequantArgs d = {};
+    d.c = c;
+    d.block_table = a.block_table;
+    d.bt_stride = a.bt_stride;
+    d.num_blocks = a.num_blocks;
+    d.block_size = a.block_size;
+    d.num_kv_heads = a.num_kv_heads;
+    d.head_dim = a.head_dim;
+    d.k = k;
+    d.v = v;
+    d.table = reinterpret_cast<int32_t*>(scratch);
+    d.error_word = a.error_word;
+    d.dst0 = dst;
+    cb::PrefillArgs pa = {};
+    pa.a = a;
+    pa.a.k_cache = k;
+    pa.a.v_cache = v;
+    pa.a.block_table = d.table;
+    pa.a.bt_stride = 1;  // an entry's "request" is the offset of its table row
+    pa.a.num_blocks = (int)total;
+    pa.tile_tokens = 128 / (a.num_q_heads / a.num_kv_heads);
+    pa.box_keys = std::min(a.block_size, 128);
+    pa.metadata_ready = 1;
+    int* header = reinterpret_cast<int*>(ws);
+    pa.exit_counter = header + cb::kExitCounterOffset / 4;
+    pa.unit_counter = header + cb::kUnitCounterOffset / 4;
+    pa.scatter_counter = header + cb::kScatterCounterOffset / 4;
+    for (int j = 0; j < n; ++j) {
+      cb::PrefillEntry e = plan.chunks[i + j];
+      const int all = (e.seq_len + a.block_size - 1) / a.block_size;
+      const int first =
+          first_key(e.seq_len - e.q_len, a.sliding_window) / 128 * 128 / a.block_size;
+      d.entries[j] = cb::DequantEntry{e.r, first, all - first, dst, row};
+      e.r = row;
+      pa.entries[j] = e;
+      pa.total_ctas += cb::prefill_ctas(e.n_qtiles, a.num_kv_heads);
+      row += all;
+      dst += all - first;
+    }
+    d.n_entries = pa.n_entries = n;
+    d.n_pages = dst - d.dst0;
+    pa.total_units = pa.total_ctas;
+    pa.grid = std::min(pa.total_units, cb::sm_count());
+    cudaError_t e = cb::launch_dequant_pages_q8(d, s);
+    if (e == cudaSuccess) e = cb::launch_prefill(pa, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cb_status check_rows(const char* what, const void* k, const void* v, const cb::Q8Cache& c,
+                     const int64_t* slot_mapping, int32_t num_tokens, int32_t num_blocks,
+                     int32_t block_size, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                     bool* empty) {
+  (void)what;
+  *empty = false;
+  if (dtype != CB_F32 && dtype != CB_BF16)
+    return report_error(CB_ERR_INVALID_ARG, "dtype must be CB_F32 or CB_BF16");
+  if (num_tokens < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 || head_dim <= 0)
+    return report_error(CB_ERR_INVALID_ARG, "sizes must be positive (num_tokens >= 0)");
+  if (head_dim != 64 && head_dim != 128)
+    return report_error(CB_ERR_UNSUPPORTED, "8-bit cache: head_dim must be 64 or 128");
+  if ((int64_t)num_tokens * num_kv_heads >= (int64_t)1 << 33)
+    return report_error(CB_ERR_UNSUPPORTED, "8-bit cache: too many rows in one call");
+  if (num_tokens == 0) {
+    *empty = true;
+    return CB_OK;
+  }
+  if (!k || !v || !c.k || !c.v || !c.k_scale || !c.v_scale || !slot_mapping)
+    return report_error(CB_ERR_INVALID_ARG, "null pointer");
+  for (const void* p : {k, v, (const void*)c.k, (const void*)c.v, (const void*)c.k_scale,
+                        (const void*)c.v_scale})
+    if (!cb::is_aligned16(p))
+      return report_error(CB_ERR_INVALID_ARG, "K/V and scale pointers must be 16-byte aligned");
+  return CB_OK;
+}
+
+cb::Q8Cache cache_of(const void* k, const void* v, const void* ks, const void* vs) {
+  auto u8 = [](const void* p) { return static_cast<uint8_t*>(const_cast<void*>(p)); };
+  return cb::Q8Cache{u8(k), u8(v), u8(ks), u8(vs)};
+}
+
+cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const void* k_new,
+                       const void* v_new, const int64_t* slot_mapping,
+                       const int32_t* query_start_loc, const int32_t* seq_lens,
+                       const int32_t* block_table, int32_t block_table_stride,
+                       const int32_t* h_query_start_loc, const int32_t* h_seq_lens,
+                       int32_t num_requests, int32_t num_tokens, int32_t num_blocks,
+                       int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                       int32_t head_dim, float scale, int32_t sliding_window, int32_t dtype,
+                       uint32_t flags, void* workspace, size_t workspace_bytes, void* stream) {
+  cb_status st = cb::check_step_sizes(num_requests, num_tokens, num_blocks, block_size, num_q_heads,
+                                      num_kv_heads, head_dim, block_table_stride, dtype,
+                                      h_query_start_loc, h_seq_lens);
+  if (st != CB_OK) return st;
+  const Layout w = layout_of(num_kv_heads, head_dim);
+  if (!workspace || workspace_bytes < w.scratch)
+    return report_error(CB_ERR_WORKSPACE, "workspace missing or smaller than cb_workspace_size_q8()");
+  if (!cb::is_aligned16(workspace))
+    return report_error(CB_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  int64_t max_pages = 0;
+  st = cb::check_step_mirrors(h_query_start_loc, h_seq_lens, num_requests, block_size, &max_pages);
+  if (st != CB_OK) return st;
+  if (h_query_start_loc[num_requests] != num_tokens)
+    return report_error(CB_ERR_METADATA, "query_start_loc[R] must equal num_tokens");
+  if (max_pages > block_table_stride)
+    return report_error(CB_ERR_METADATA,
+                        "block_table_stride is smaller than ceil(seq_len / block_size)");
+  if (num_tokens == 0) return CB_OK;
+  if (!out || !q || !c.k || !c.v || !c.k_scale || !c.v_scale || !query_start_loc || !seq_lens ||
+      !block_table)
+    return report_error(CB_ERR_INVALID_ARG, "null pointer");
+  if (k_new && (!v_new || !slot_mapping))
+    return report_error(CB_ERR_INVALID_ARG, "k_new given without v_new or slot_mapping");
+  for (const void* p : {(const void*)out, q, (const void*)c.k, (const void*)c.v,
+                        (const void*)c.k_scale, (const void*)c.v_scale, k_new, v_new})
+    if (!cb::is_aligned16(p))
+      return report_error(CB_ERR_INVALID_ARG, "q/out/K/V/scale pointers must be 16-byte aligned");
+
+  cb::StepArgs a = {};
+  a.out = out;
+  a.q = q;
+  a.query_start_loc = query_start_loc;
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.bt_stride = block_table_stride;
+  a.num_requests = num_requests;
+  a.num_tokens = num_tokens;
+  a.num_blocks = num_blocks;
+  a.block_size = block_size;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)head_dim)) * 1.4426950408889634f;
+  a.sliding_window = sliding_window > 0 ? sliding_window : 0;
+  a.dtype = dtype;
+  a.error_word = static_cast<int32_t*>(workspace);
+
+  // a 16-key block lies in one page from block_size 16 on; the rest runs on the portable kernel
+  const bool fast = block_size % cb::kQ8KeyBlock == 0 && !(flags & CB_FLAG_PORTABLE_ONLY);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  static thread_local Q8Plan plan;  // its vectors keep their storage from call to call
+  plan.split = false;
+  plan.merge.clear();
+  plan.chunks.clear();
+  plan.max_pieces = 0;
+  if (fast) {
+    const int G = num_q_heads / num_kv_heads;
+    const int max_q = dtype == CB_F32 ? INT_MAX : std::max(1, kChunkColumns / G);
+    const size_t need = plan_chunks(plan, a, max_q, h_query_start_loc, h_seq_lens);
+    if (need > workspace_bytes - w.scratch)
+      return report_error(CB_ERR_WORKSPACE,
+                          "workspace too small for the step's chunks: chunk_kv_tokens of "
+                          "cb_workspace_size_q8() must cover the seq_lens of requests with q_len > 1");
+    plan_split(plan, a, c, max_q, h_query_start_loc, h_seq_lens, ws);
+  }
+  cudaError_t e = cudaSuccess;
+  if (k_new)
+    e = cb::launch_write_kv_q8(k_new, v_new, c, slot_mapping, num_tokens,
+                               (int64_t)num_blocks * block_size, num_kv_heads, head_dim, dtype,
+                               a.error_word, s);
+  if (e != cudaSuccess) return cb::report_cuda_error(e, "write_kv_q8 launch");
+  if (!fast) {
+    e = cb::launch_q8_portable(a, c, s);
+  } else {
+    if (plan.split) e = cb::launch_q8_split(plan.args, plan.column_blocks, s);
+    if (e == cudaSuccess && !plan.merge.empty()) {
+      cb::MergeArgs m;
+      m.out = out;
+      m.dtype = dtype;
+      m.num_q_heads = num_q_heads;
+      m.head_dim = head_dim;
+      m.part_o = plan.args.part_o;
+      m.part_ml = plan.args.part_ml;
+      m.parts = cb::merge_parts(plan.max_pieces);
+      e = cb::launch_merge(m, plan.merge.data(), (int)plan.merge.size(), s);
+    }
+    if (e == cudaSuccess && !plan.chunks.empty()) e = run_chunks(plan, a, c, ws, s);
+  }
+  if (e != cudaSuccess) return cb::report_cuda_error(e, "8-bit attention launch");
+  return CB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+cb_status cb_write_kv_q8(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
+                         void* k_scale, void* v_scale, const int64_t* slot_mapping,
+                         int32_t num_tokens, int32_t num_blocks, int32_t block_size,
+                         int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                         int32_t* error_word, void* stream) {
+  const cb::Q8Cache c = cache_of(k_cache, v_cache, k_scale, v_scale);
+  bool empty = false;
+  const cb_status st = check_rows("write", k_new, v_new, c, slot_mapping, num_tokens, num_blocks,
+                                  block_size, num_kv_heads, head_dim, dtype, &empty);
+  if (st != CB_OK || empty) return st;
+  const cudaError_t e = cb::launch_write_kv_q8(
+      k_new, v_new, c, slot_mapping, num_tokens, (int64_t)num_blocks * block_size, num_kv_heads,
+      head_dim, dtype, error_word, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CB_OK : cb::report_cuda_error(e, "write_kv_q8 launch");
+}
+
+cb_status cb_read_kv_q8(const void* k_cache, const void* v_cache, const void* k_scale,
+                        const void* v_scale, const int64_t* slot_mapping, void* k_out,
+                        void* v_out, int32_t num_tokens, int32_t num_blocks, int32_t block_size,
+                        int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                        int32_t* error_word, void* stream) {
+  const cb::Q8Cache c = cache_of(k_cache, v_cache, k_scale, v_scale);
+  bool empty = false;
+  const cb_status st = check_rows("read", k_out, v_out, c, slot_mapping, num_tokens, num_blocks,
+                                  block_size, num_kv_heads, head_dim, dtype, &empty);
+  if (st != CB_OK || empty) return st;
+  const cudaError_t e = cb::launch_read_kv_q8(
+      k_out, v_out, c, slot_mapping, num_tokens, (int64_t)num_blocks * block_size, num_kv_heads,
+      head_dim, dtype, error_word, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CB_OK : cb::report_cuda_error(e, "read_kv_q8 launch");
+}
+
+size_t cb_workspace_size_q8(int32_t num_requests, int32_t num_tokens, int32_t num_q_heads,
+                            int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                            int64_t chunk_kv_tokens) {
+  (void)num_tokens;
+  if (num_requests < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      block_size <= 0)
+    return cb::kWorkspaceHeaderBytes;
+  const size_t fixed = layout_of(num_kv_heads, head_dim).scratch;
+  if (chunk_kv_tokens <= 0) return fixed;
+  // each request's pages are rounded up
+  const int64_t pages = chunk_kv_tokens / block_size + std::min<int64_t>(num_requests, chunk_kv_tokens);
+  return fixed + scratch_bytes(pages, pages, block_size, num_kv_heads, head_dim);
+}
+
+cb_status cb_paged_attention_q8(void* out, const void* q, void* k_cache, void* v_cache,
+                                void* k_scale, void* v_scale, const void* k_new,
+                                const void* v_new, const int64_t* slot_mapping,
+                                const int32_t* query_start_loc, const int32_t* seq_lens,
+                                const int32_t* block_table, int32_t block_table_stride,
+                                const int32_t* h_query_start_loc, const int32_t* h_seq_lens,
+                                int32_t num_requests, int32_t num_tokens, int32_t num_blocks,
+                                int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                                int32_t head_dim, float scale, int32_t sliding_window,
+                                int32_t dtype, uint32_t flags, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  try {
+    return attention_q8(out, q, cache_of(k_cache, v_cache, k_scale, v_scale), k_new, v_new,
+                        slot_mapping, query_start_loc, seq_lens, block_table, block_table_stride,
+                        h_query_start_loc, h_seq_lens, num_requests, num_tokens, num_blocks,
+                        block_size, num_q_heads, num_kv_heads, head_dim, scale, sliding_window,
+                        dtype, flags, workspace, workspace_bytes, stream);
+  } catch (...) {  // host memory ran out while planning; nothing was launched
+    return report_error(CB_ERR_INVALID_ARG, "out of host memory");
+  }
+}
+
+}  // extern "C"
