@@ -72,6 +72,10 @@ typedef enum cb_dtype { CB_F32 = 0, CB_BF16 = 1 } cb_dtype;
  * on that workspace. */
 #define CB_FLAG_TEST_WAIT_EXPIRY 0x2u
 
+/* cb_paged_attention_shared: share every prefix that can be, also where it would not pay (for
+ * tests and measurements of that choice). */
+#define CB_FLAG_SHARE_ALWAYS 0x4u
+
 /* Error-word codes recorded on the device (bit set). */
 #define CB_DEVERR_BLOCK_ID 0x1 /* a block_table entry outside [0, num_blocks) */
 #define CB_DEVERR_SLOT 0x2     /* a slot_mapping entry >= num_blocks * block_size */
@@ -436,6 +440,42 @@ cb_status cb_paged_attention_q8(void* out, const void* q, void* k_cache, void* v
                                 int32_t head_dim, float scale, int32_t sliding_window,
                                 int32_t dtype, uint32_t flags, void* workspace,
                                 size_t workspace_bytes, void* stream);
+
+/* ---- shared prefixes ---------------------------------------------------- */
+
+/*
+ * cb_paged_attention_shared -- the step of cb_paged_attention for batches in which groups of
+ * requests share a prompt prefix held once in the pool: the same leading block-table entries
+ * ("Continuous batching architecture", Transformers docs, section "Prefix caching": full blocks
+ * shared between requests with the same prefix). The result is cb_paged_attention's on the same
+ * arguments; the prefix is attended once for all of a group's decode rows, as a dense product,
+ * instead of once per request, and joined with each row's own suffix by log-sum-exp.
+ *
+ * Group g is the requests h_group_start[g] .. h_group_start[g + 1] - 1 (host, [num_groups + 1],
+ * from 0 to num_requests). prefix_lens (device [R] int32) and its host mirror h_prefix_lens: the
+ * positions of request r that it shares with the rest of its group: whole blocks, at most its
+ * context seq_len - q_len, equal over a group's requests with q_len > 0, and 0 for requests with
+ * q_len > 1 (CB_ERR_METADATA otherwise). 0 shares nothing. The first prefix_lens[r] / block_size
+ * block-table entries of a group's requests must be the same pages: those of one of the
+ * requests are read for all. num_groups 0 is the plain step (prefix_lens may be NULL).
+ * The step's new rows must not be written into shared pages (they never are: a prefix is part of
+ * the context).
+ *
+ * Everything else is as for cb_paged_attention. Steps in fp32, with a sliding window, on block
+ * sizes below 8, with more than 128 groups, or whose groups are so small that sharing would not
+ * pay, run as the plain step. workspace: at least cb_workspace_size_shared(...) bytes.
+ */
+size_t cb_workspace_size_shared(int32_t num_requests, int32_t num_tokens, int32_t num_q_heads,
+                                int32_t num_kv_heads, int32_t head_dim);
+cb_status cb_paged_attention_shared(
+    void* out, const void* q, void* k_cache, void* v_cache, const void* k_new, const void* v_new,
+    const int64_t* slot_mapping, const int32_t* query_start_loc, const int32_t* seq_lens,
+    const int32_t* block_table, int32_t block_table_stride, const int32_t* prefix_lens,
+    const int32_t* h_query_start_loc, const int32_t* h_seq_lens, const int32_t* h_prefix_lens,
+    const int32_t* h_group_start, int32_t num_groups, int32_t num_requests, int32_t num_tokens,
+    int32_t num_blocks, int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, float scale, int32_t sliding_window, int32_t dtype, uint32_t flags,
+    void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- diagnostics (no effect on results) -------------------------------- */
 

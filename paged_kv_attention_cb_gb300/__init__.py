@@ -18,6 +18,7 @@ CB_F32 = 0
 CB_BF16 = 1
 CB_FLAG_PORTABLE_ONLY = 0x1
 CB_FLAG_TEST_WAIT_EXPIRY = 0x2  # tests of the failure path only (see include/cb.h)
+CB_FLAG_SHARE_ALWAYS = 0x4  # paged_attention_shared: share also where it would not pay
 CB_DEVERR_BLOCK_ID = 0x1
 CB_DEVERR_SLOT = 0x2
 CB_DEVERR_TIMEOUT = 0x4
@@ -79,6 +80,9 @@ _SIGNATURES = {
     "cb_read_kv_q8": (ctypes.c_int, [_vp] * 7 + [_i32] * 6 + [_vp, _vp]),
     "cb_workspace_size_q8": (ctypes.c_size_t, [_i32] * 6 + [ctypes.c_int64]),
     "cb_paged_attention_q8": (ctypes.c_int, [_vp] * 12 + [_i32, _vp, _vp] + [_i32] * 7 + [
+        ctypes.c_float, _i32, _i32, ctypes.c_uint32, _vp, ctypes.c_size_t, _vp]),
+    "cb_workspace_size_shared": (ctypes.c_size_t, [_i32] * 5),
+    "cb_paged_attention_shared": (ctypes.c_int, [_vp] * 10 + [_i32] + [_vp] * 5 + [_i32] * 8 + [
         ctypes.c_float, _i32, _i32, ctypes.c_uint32, _vp, ctypes.c_size_t, _vp]),
     "cb_launch_count": (ctypes.c_longlong, [ctypes.c_int]),
     "cb_num_kernels": (ctypes.c_int, []),
@@ -515,6 +519,60 @@ def paged_attention_q8(out, q, k_cache, v_cache, k_scale, v_scale, query_start_l
             hq.ctypes.data, hs.ctypes.data, R, T, NB, BS, Hq, Hkv, D, float(scale),
             int(sliding_window), _dtype_code(q), int(flags), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
+    return out
+
+
+# ---------------------------------------------------------------- shared prefixes
+
+
+def workspace_size_shared(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim) -> int:
+    return int(lib().cb_workspace_size_shared(num_requests, num_tokens, num_q_heads, num_kv_heads,
+                                              head_dim))
+
+
+def alloc_workspace_shared(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                           device="cuda"):
+    """Allocate (with torch) and zero a workspace of cb_workspace_size_shared bytes."""
+    import torch
+
+    n = workspace_size_shared(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim)
+    return torch.zeros((n + 15) // 16 * 16, dtype=torch.uint8, device=device)
+
+
+def paged_attention_shared(out, q, k_cache, v_cache, query_start_loc, seq_lens, block_table,
+                           prefix_lens, h_query_start_loc, h_seq_lens, h_prefix_lens,
+                           h_group_start, workspace, *, scale=0.0, sliding_window=0, k_new=None,
+                           v_new=None, slot_mapping=None, flags=0, stream=None):
+    """paged_attention for groups of requests that share a prompt prefix (see
+    cb_paged_attention_shared in include/cb.h).
+
+    prefix_lens [R] int32 on the device and h_prefix_lens on the host: positions each request
+    shares with its group; h_group_start [n_groups + 1] on the host: group g is the requests
+    h_group_start[g] .. h_group_start[g + 1] - 1. workspace: alloc_workspace_shared.
+    """
+    Hkv = k_cache.shape[2] if k_cache.dim() == 4 else 0
+    T, Hq, D, R, stride, hq, hs, dev = _step_checks(
+        out, q, Hkv, query_start_loc, seq_lens, block_table, h_query_start_loc, h_seq_lens, k_new,
+        v_new, slot_mapping, workspace)
+    shape = k_cache.shape
+    if len(shape) != 4 or shape[3] != D:
+        raise CbError(1, f"k_cache: shape {tuple(shape)}, not [num_blocks, block_size, Hkv, {D}]")
+    kinds = (q.dtype,)
+    _need(k_cache, "k_cache", shape, kinds, dev)
+    _need(v_cache, "v_cache", shape, kinds, dev)
+    _need(prefix_lens, "prefix_lens", (R,), _I32, dev)
+    hp, hg = _host_i32(h_prefix_lens), _host_i32(h_group_start)
+    if hp.shape != (R,) or hg.ndim != 1 or not len(hg):
+        raise CbError(2, "h_prefix_lens must have R entries, h_group_start n_groups + 1")
+    with _on(dev):
+        _check(lib().cb_paged_attention_shared(
+            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_new),
+            _ptr(v_new), _ptr(slot_mapping), query_start_loc.data_ptr(), seq_lens.data_ptr(),
+            block_table.data_ptr(), stride, prefix_lens.data_ptr(), hq.ctypes.data,
+            hs.ctypes.data, hp.ctypes.data, hg.ctypes.data, len(hg) - 1, R, T, shape[0], shape[1],
+            Hq, Hkv, D, float(scale), int(sliding_window), _dtype_code(q), int(flags),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _stream_on(stream, dev)))
     return out
 
 

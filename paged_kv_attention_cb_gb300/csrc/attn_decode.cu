@@ -60,7 +60,7 @@ struct SegDesc {
   int lo;      // first attended key (window start)
   int hi;      // last attended key (= seq_len - 1)
   int slot;    // partial slot (r + CTA index)
-  int direct;  // 1: the request lies wholly in this CTA
+  int direct;  // 1: the request lies wholly in this CTA (and no part of it elsewhere)
 };
 
 struct DecodeSmem {
@@ -77,10 +77,11 @@ struct DecodeSmem {
   int abort_flag;
 };
 
-CB_DEV int kb_lo_of(int seq, int window) {
-  const int lo = window > 0 ? max(0, seq - window) : 0;
-  return lo / kKB;
+CB_DEV int key_lo_of(int seq, int window, int start) {
+  return window > 0 ? max(start, seq - window) : start;
 }
+
+CB_DEV int kb_lo_of(int seq, int window, int start) { return key_lo_of(seq, window, start) / kKB; }
 
 // Row of (local head hl, key k of the 16-key block) in a staged K or V half: (head, key)
 // for pages of 16 keys or more, (page, head, key) for 8-key pages. Rows are 128 bytes
@@ -90,18 +91,22 @@ CB_DEV int stage_row(bool pages8, int hb, int hl, int k) {
 }
 
 // Key blocks a decode query of a request of seq_len `seq` attends.
-CB_DEV int units_of(int seq, int window) { return (seq - 1) / kKB - kb_lo_of(seq, window) + 1; }
+CB_DEV int units_of(int seq, int window, int start) {
+  return (seq - 1) / kKB - kb_lo_of(seq, window, start) + 1;
+}
 
 // Key blocks of request r if it is a decode request, else 0.
-// (The three loads are independent: one memory round trip.)
-CB_DEV int decode_units(const StepArgs& a, int r, int* seq_out, int* t_out) {
+// (The loads are independent: one memory round trip.)
+CB_DEV int decode_units(const StepArgs& a, int r, int* seq_out, int* t_out, int* start_out) {
   const int q0 = __ldg(a.query_start_loc + r);
   const int q1 = __ldg(a.query_start_loc + r + 1);
   const int seq = __ldg(a.seq_lens + r);
+  const int start = a.kv_start != nullptr ? __ldg(a.kv_start + r) : 0;
   *seq_out = seq;
   *t_out = q0;
+  *start_out = start;
   if (q1 - q0 != 1 || seq <= 0) return 0;
-  return units_of(seq, a.sliding_window);
+  return units_of(seq, a.sliding_window, start);
 }
 
 // CTAs a partition of U key blocks uses out of a launch of C: at least
@@ -186,8 +191,8 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // the decode requests' key blocks, summed over the step from the device metadata
     long long part = 0;
     for (int r = threadIdx.x; r < R; r += nthreads) {
-      int seq = 0, t = 0;
-      part += decode_units(p.a, r, &seq, &t);
+      int seq = 0, t = 0, start = 0;
+      part += decode_units(p.a, r, &seq, &t, &start);
     }
     part = warp_incl_scan(part);
     if (lane == 31) sm.scan[warp] = part;
@@ -220,8 +225,8 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
     long long carry = 0;
     for (int base_r = 0; base_r < R; base_r += nthreads) {
       const int r = base_r + threadIdx.x;
-      int seq = 0, t = 0, units = 0;
-      if (r < R) units = decode_units(p.a, r, &seq, &t);
+      int seq = 0, t = 0, start = 0, units = 0;
+      if (r < R) units = decode_units(p.a, r, &seq, &t, &start);
       long long v = warp_incl_scan(units);
       if (lane == 31) sm.scan[warp] = v;
       __syncthreads();
@@ -266,15 +271,16 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const uint64_t kv_policy = l2_policy_evict_first();
 
     bool ok = true;
-    int wbase = -1, w_units = 0, w_seq = 0, w_t = 0;
+    int wbase = -1, w_units = 0, w_seq = 0, w_t = 0, w_start = 0;
     auto load_window = [&](int r0) {
       wbase = r0;
       const int r = r0 + lane;
-      int seq = 0, t = 0, units = 0;
-      if (r < R) units = decode_units(p.a, r, &seq, &t);
+      int seq = 0, t = 0, start = 0, units = 0;
+      if (r < R) units = decode_units(p.a, r, &seq, &t, &start);
       w_units = units;
       w_seq = seq;
       w_t = t;
+      w_start = start;
     };
     // next decode request at or after r (R when none)
     auto next_decode = [&](int r) -> int {
@@ -304,13 +310,14 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       return pg;
     };
     // walk state of the current segment
-    int r = -1, seq = 0, t = 0, units = 0;
+    int r = -1, seq = 0, t = 0, start = 0, units = 0;
     long long u_r = 0, u = u_lo;
     auto fetch = [&](int rr) {
       const int j = rr - wbase;
       units = __shfl_sync(0xffffffffu, w_units, j);
       seq = __shfl_sync(0xffffffffu, w_seq, j);
       t = __shfl_sync(0xffffffffu, w_t, j);
+      start = __shfl_sync(0xffffffffu, w_start, j);
     };
     int kb0 = 0, kb1 = 0;
     int pages = 0;  // page ids of the batch about to be issued (lane j: key block kb + j)
@@ -326,14 +333,15 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
         kb1 = c.kb1;
         t = c.t;
         seq = c.seq;
-        units = units_of(seq, p.a.sliding_window);
+        start = c.start;
+        units = units_of(seq, p.a.sliding_window, start);
         pages = load_pages(r, kb0, min(32, kb1 - kb0), seq);
         pages2 = pg2_next;
         load_window(r);
       } else {
         load_window(r);
         fetch(r);
-        const int kbl = kb_lo_of(seq, p.a.sliding_window);
+        const int kbl = kb_lo_of(seq, p.a.sliding_window, start);
         kb0 = kbl + (int)(u - u_r);
         kb1 = kbl + (int)(min(u_r + units, u_hi) - u_r);
         pages = load_pages(r, kb0, min(32, kb1 - kb0), seq);
@@ -356,10 +364,10 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
         d.kb0 = kb0;
         d.kb1 = kb1;
         d.t = t;
-        d.lo = p.a.sliding_window > 0 ? max(0, seq - p.a.sliding_window) : 0;
+        d.lo = key_lo_of(seq, p.a.sliding_window, start);
         d.hi = seq - 1;
         d.slot = r + b;
-        d.direct = (b_first == b_last);
+        d.direct = (b_first == b_last) && start == 0;
         mbar_arrive_expect_tx(&sm.qfull[qs], q_bytes);
         bulk_load(qring + qs * p.q_slot_bytes,
                   q + (long long)t * q_row_elems + (long long)hg * HB * G * D, q_bytes,
@@ -442,7 +450,8 @@ decode_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const int jn = nr - wbase;
                 const int n_units = __shfl_sync(0xffffffffu, w_units, jn);
                 const int n_seq = __shfl_sync(0xffffffffu, w_seq, jn);
-                const int nkbl = kb_lo_of(n_seq, p.a.sliding_window);
+                const int n_start = __shfl_sync(0xffffffffu, w_start, jn);
+                const int nkbl = kb_lo_of(n_seq, p.a.sliding_window, n_start);
                 nkb0 = nkbl;
                 nkb1 = nkbl + (int)(min(nu_r + n_units, u_hi) - nu_r);
                 pages = load_pages(nr, nkb0, min(32, nkb1 - nkb0), n_seq);
@@ -779,8 +788,8 @@ decode_combine_kernel(const CombineArgs c) {
     if (r >= a.num_requests) return;
     long long all = 0, before = 0;
     for (int i = threadIdx.x; i < a.num_requests; i += nthreads) {
-      int sq = 0, tt = 0;
-      const int u = decode_units(a, i, &sq, &tt);
+      int sq = 0, tt = 0, st = 0;
+      const int u = decode_units(a, i, &sq, &tt, &st);
       all += u;
       if (i < r) before += u;
     }
@@ -797,8 +806,8 @@ decode_combine_kernel(const CombineArgs c) {
       }
       __syncthreads();
     }
-    int seq = 0;
-    const int units = decode_units(a, r, &seq, &t);
+    int seq = 0, start = 0;
+    const int units = decode_units(a, r, &seq, &t, &start);
     const long long U = totals[0];
     if (units == 0 || U == 0) return;
     const int C = decode_ctas_used(U, c.num_ctas);

@@ -50,6 +50,8 @@
 #include <cudaTypedefs.h>
 #include <float.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 #include "prefill.h"
@@ -185,6 +187,65 @@ CB_DEV Work work_of(const PrefillArgs& p, int cta) {
   return Work{-1, 0, 0};
 }
 
+// Shared-prefix units: index -> (entry, KV head, pair of query tiles, split of the key tiles),
+// the pairs that read the same keys next to each other. `pair` carries the split above bit 16.
+CB_DEV Work work_of(const PrefixArgs& p, int cta) {
+  const int Hkv = p.a.num_kv_heads;
+  int base = 0;
+  for (int e = 0; e < p.n_entries; ++e) {
+    const int npairs = (p.entries[e].n_qtiles + 1) / 2;
+    const int splits = (((p.entries[e].seq_len + kKeys - 1) / kKeys) + p.tiles_per_unit - 1) / p.tiles_per_unit;
+    const int n = npairs * Hkv * splits;
+    if (cta < base + n) {
+      const int k = cta - base;
+      return Work{e, k / npairs % Hkv, k % npairs | (k / (npairs * Hkv)) << 16};
+    }
+    base += n;
+  }
+  return Work{-1, 0, 0};
+}
+
+// A shared-prefix unit (its descriptor's r is the entry): the prefix as a context without new
+// tokens, so that every row attends all of it, and of its key tiles those of the unit's split.
+CB_DEV Geo geo_of(const PrefixArgs& p, const UnitDesc& d, int TQ) {
+  Geo e;
+  e.r = p.entries[d.r].r;
+  e.g = d.g;
+  e.q_start = d.q_start;
+  e.q_len = d.q_len;
+  e.seq = d.seq_len;
+  e.ctx = d.seq_len;
+  e.qt0 = kTiles * (d.pair & 0xffff);
+  e.has_b = e.qt0 + 1 < (d.q_len + TQ - 1) / TQ;
+  e.tok0 = e.qt0 * TQ;
+  e.tok_end = min(d.q_len, e.tok0 + kTiles * TQ);
+  e.kt0 = (d.pair >> 16) * p.tiles_per_unit;
+  e.nkt = min(p.tiles_per_unit, (d.seq_len + kKeys - 1) / kKeys - e.kt0);
+  return e;
+}
+
+// Transpose of 32-byte pieces within each group of four lanes: piece k (words 8k .. 8k + 7) of
+// lane 4a + q becomes piece q of lane 4a + k. At lane distance d, the lane whose bit d is set
+// swaps its pieces with bit d clear for its partner's pieces with bit d set.
+CB_DEV void quad_transpose(uint32_t (&w)[32], int lane) {
+#pragma unroll
+  for (int d = 2; d >= 1; d >>= 1) {
+    const bool hi = (lane & d) != 0;
+#pragma unroll
+    for (int k0 = 0; k0 < 4; ++k0) {
+      if (k0 & d) continue;
+      const int k1 = k0 | d;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t x = hi ? w[8 * k0 + i] : w[8 * k1 + i];
+        const uint32_t y = __shfl_xor_sync(0xffffffffu, x, d);
+        if (hi) w[8 * k0 + i] = y;
+        else w[8 * k1 + i] = y;
+      }
+    }
+  }
+}
+
 // The pages of key tile `key_base` in `gen` (bit i: page i of the tile), row by row into
 // the ring slot `dst` (128B-swizzled rows of 64 of head_dim per half): a new position whose
 // slot is its own (bit clear in `bad`) from the step's new rows, any other from its cache
@@ -241,14 +302,15 @@ __device__ __noinline__ void copy_rows(uint8_t* dst, unsigned gen, int ids_cur, 
 
 }  // namespace
 
-template <int D>
+// kShared: over the shared prefixes of groups of decode rows (PrefixArgs), into partial rows.
+template <int D, bool kShared>
 __global__ void __launch_bounds__(kThreadsBound, 1)
 prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v,
                     const __grid_constant__ CUtensorMap tmap_kn,
                     const __grid_constant__ CUtensorMap tmap_vn,
                     const __grid_constant__ CUtensorMap tmap_q,
-                    const __grid_constant__ PrefillArgs p) {
+                    const __grid_constant__ std::conditional_t<kShared, PrefixArgs, PrefillArgs> p) {
   static_assert(D == 64 || D == 128, "head_dim");
   constexpr int kHalves = D / 64;
   constexpr int kTile = tile_bytes<D>();
@@ -271,7 +333,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
   // Graph replays: the one unit of this CTA, found with a block scan over the device
   // metadata (request order; each request with q_len > 1 has ceil(n_qtiles / 2) * Hkv).
   __shared__ UnitDesc s_first;  // the unit found on the device (kept out of registers)
-  if (p.device_work) {
+  if (!kShared && p.device_work) {
     grid_dependency_wait();
     __shared__ int s_tot[kThreads / 32];
     __shared__ int s_hit[2];
@@ -399,6 +461,10 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
   // next unit of the step's list (heaviest first) claimed through an atomic counter, so
   // that a CTA takes a new unit as soon as it can (and CTAs that start late, on SMs a
   // decode grid held, take what is left).
+  auto unit_geo = [&](const UnitDesc& d) -> Geo {
+    if constexpr (kShared) return geo_of(p, d, TQ);
+    else return geo_of(d, TQ, W);
+  };
   auto read_unit = [&](int u, UnitDesc& d) -> bool {
     if (!mbar_wait_warp_or_abort(&bar.unit_full[u & 1], (uint32_t)((u >> 1) & 1), &bar.abort))
       return false;
@@ -456,7 +522,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
             const Work w = work_of(p, idx);
             if (w.e >= 0) {
               const PrefillEntry& en = p.entries[w.e];
-              d = UnitDesc{en.r, en.q_start, en.q_len, en.seq_len, w.g, w.pair, 1};
+              d = UnitDesc{kShared ? w.e : en.r, en.q_start, en.q_len, en.seq_len, w.g, w.pair, 1};
             }
           }
         }
@@ -470,7 +536,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         break;
       }
       if (!d.live) break;
-      const Geo e = geo_of(d, TQ, W);
+      const Geo e = unit_geo(d);
       const int g = e.g, q_start = e.q_start, seq = e.seq, ctx = e.ctx, kt0 = e.kt0, nkt = e.nkt;
       const int npages_req = (seq + BS - 1) / BS;
       const int32_t* bt = p.a.block_table + (long long)e.r * p.a.bt_stride;
@@ -655,7 +721,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         break;
       }
       if (!d.live) break;
-      const Geo e = geo_of(d, TQ, W);
+      const Geo e = unit_geo(d);
       const int nkt = e.nkt;
       const bool has_b = e.has_b;
       ok = mbar_wait_warp_or_abort(&bar.q_full, (uint32_t)(u & 1), &bar.abort) && slot_ready(i_base);
@@ -727,7 +793,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const uint32_t tO = tmem + lane_addr + 2 * kKeys + t * D;
     int i_base = 0;
     int swaits = 0;  // s_full[t] waits so far (phase parity)
-    const bool copy_rows_after = p.k_new != nullptr && !p.device_work;  // the row copy below
+    const bool copy_rows_after = !kShared && p.k_new != nullptr && !p.device_work;  // the row copy below
     bool claimed = false;  // its first part is claimed already (lane 0: first_part)
     int first_part = 0;
     int owaits = 0;  // o_done[t] waits so far
@@ -740,7 +806,8 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         break;
       }
       const volatile UnitDesc* ud = &bar.unit[u & 1];
-#define CB_UNIT_GEO() geo_of(ud->r, ud->q_start, ud->q_len, ud->seq_len, ud->g, ud->pair, TQ, W)
+#define CB_UNIT_GEO() \
+  unit_geo(UnitDesc{ud->r, ud->q_start, ud->q_len, ud->seq_len, ud->g, ud->pair, 1})
 #define CB_RELEASE_UNIT()                                 \
   do {                                                    \
     __syncwarp();                                         \
@@ -879,7 +946,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
       // ---- epilogue: O / l for the rows of this tile. The rows' output offsets are
       // computed while the last PV product runs (~600 cycles after the wait otherwise).
       const int q4 = lane & 3;
-      long long orow[4];  // bf16 offset of rows 4a .. 4a + 3 of the warp, -1 past q_len
+      long long orow[4];  // output offset of rows 4a .. 4a + 3 of the warp, -1 past q_len
       {
         const Geo e = CB_UNIT_GEO();
         const int lg = __ffs(G) - 1;
@@ -887,9 +954,15 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         for (int s4 = 0; s4 < 4; ++s4) {
           const int r = (warp & 3) * 32 + 4 * (lane >> 2) + s4;  // tile row
           const int tok = (e.qt0 + t) * TQ + (r >> lg);
-          orow[s4] = tok < e.q_len ? ((long long)(e.q_start + tok) * p.a.num_q_heads + e.g * G +
-                                      (r & (G - 1))) * D + q4 * 16
-                                   : -1;
+          if constexpr (kShared) {  // offset in the partial rows, four fp32 pieces a line
+            const long long base = (long long)p.part_row[ud->r] + (ud->pair >> 16) * e.q_len;
+            orow[s4] = tok < e.q_len ? ((base + tok) * p.a.num_q_heads + e.g * G + (r & (G - 1))) * D + q4 * 8
+                                     : -1;
+          } else {
+            orow[s4] = tok < e.q_len ? ((long long)(e.q_start + tok) * p.a.num_q_heads + e.g * G +
+                                        (r & (G - 1))) * D + q4 * 16
+                                     : -1;
+          }
         }
       }
       // When the next unit is already published as the end of the list, the first part of
@@ -908,6 +981,28 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         ok = false;
       if (ok) {
         tcgen05_fence_after();
+        if constexpr (kShared) {
+          // the unnormalised O and the row's statistics, as fp32 partial rows: the same in-quad
+          // transpose of 32-byte pieces, 32 columns (one 128-byte line) at a time
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t w[32];
+            tmem_ld32(tO + c0, w);
+            tmem_wait_ld();
+            quad_transpose(w, lane);
+#pragma unroll
+            for (int s4 = 0; s4 < 4; ++s4) {
+              if (orow[s4] < 0) continue;
+              st_global_v8(p.part_o + orow[s4] + c0, w[8 * s4 + 0], w[8 * s4 + 1], w[8 * s4 + 2], w[8 * s4 + 3],
+                           w[8 * s4 + 4], w[8 * s4 + 5], w[8 * s4 + 6], w[8 * s4 + 7]);
+            }
+          }
+          const int tok = kTiles * (ud->pair & 0xffff) * TQ + t * TQ + row / G;
+          const int n = ud->q_len;
+          if (tok < n)
+            p.part_ml[((long long)p.part_row[ud->r] + (ud->pair >> 16) * n + tok) * p.a.num_q_heads +
+                      ud->g * G + (row & (G - 1))] = make_float2(m_ref, l);
+        } else {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         // O / l as bf16 in whole 128-byte lines. Each lane holds its own row (TMEM lane =
         // row); a transpose of 32-byte pieces within each group of four lanes gives lane
@@ -928,24 +1023,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
             w[i] = pack_bf16x2(__uint_as_float(o0[2 * i]) * inv, __uint_as_float(o0[2 * i + 1]) * inv);
             w[16 + i] = pack_bf16x2(__uint_as_float(o1[2 * i]) * inv, __uint_as_float(o1[2 * i + 1]) * inv);
           }
-          // in-quad transpose: at lane distance d, the lane whose bit d is set swaps its
-          // pieces with bit d clear for its partner's pieces with bit d set
-#pragma unroll
-          for (int d = 2; d >= 1; d >>= 1) {
-            const bool hi = (lane & d) != 0;
-#pragma unroll
-            for (int k0 = 0; k0 < 4; ++k0) {
-              if (k0 & d) continue;
-              const int k1 = k0 | d;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const uint32_t x = hi ? w[8 * k0 + i] : w[8 * k1 + i];
-                const uint32_t y = __shfl_xor_sync(0xffffffffu, x, d);
-                if (hi) w[8 * k0 + i] = y;
-                else w[8 * k1 + i] = y;
-              }
-            }
-          }
+          quad_transpose(w, lane);
           // now piece s4 of this lane = columns c0 + 16 q .. + 15 of row 4a + s4
 #pragma unroll
           for (int s4 = 0; s4 < 4; ++s4) {
@@ -959,6 +1037,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
               *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[8 * s4 + 4], w[8 * s4 + 5], w[8 * s4 + 6], w[8 * s4 + 7]);
             }
           }
+        }
         }
         // O_t is read: the next unit's products may overwrite it
         tcgen05_fence_before();
@@ -1068,8 +1147,8 @@ cudaError_t encode(CUtensorMap* map, void* ptr, int rank, const cuuint64_t* dims
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D>
-cudaError_t launch_d(const PrefillArgs& p, cudaStream_t s) {
+template <int D, bool kShared>
+cudaError_t launch_d(const std::conditional_t<kShared, PrefixArgs, PrefillArgs>& p, cudaStream_t s) {
   const StepArgs& a = p.a;
   const cuuint64_t e = 2;
   CUtensorMap mk, mv;
@@ -1106,7 +1185,7 @@ cudaError_t launch_d(const PrefillArgs& p, cudaStream_t s) {
     err = encode(&mq, const_cast<void*>(a.q), 3, qd, qs, qb);
     if (err != cudaSuccess) return err;
   }
-  auto kern = prefill_tile_kernel<D>;
+  auto kern = prefill_tile_kernel<D, kShared>;
   static bool attr_set = false;
   constexpr size_t smem = smem_bytes<D>();
   if (!attr_set) {
@@ -1120,7 +1199,7 @@ cudaError_t launch_d(const PrefillArgs& p, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     attr_set = true;
   }
-  return launch_pdl(kPrefillTc, kern, dim3(p.grid), dim3(kThreads), smem, s, mk, mv, mkn, mvn,
+  return launch_pdl(kShared ? kPrefixTc : kPrefillTc, kern, dim3(p.grid), dim3(kThreads), smem, s, mk, mv, mkn, mvn,
                     mq, p);
 }
 
@@ -1144,16 +1223,22 @@ int prefill_ctas_bound(int num_tokens, int num_requests, int tile_tokens, int nu
 
 cudaError_t prepare_prefill(int head_dim) {
   if (head_dim == 64)
-    return cudaFuncSetAttribute(prefill_tile_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(prefill_tile_kernel<64, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem_bytes<64>());
-  return cudaFuncSetAttribute(prefill_tile_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(prefill_tile_kernel<128, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)smem_bytes<128>());
 }
 
 cudaError_t launch_prefill(const PrefillArgs& p, cudaStream_t stream) {
   if (p.grid <= 0) return cudaSuccess;
-  if (p.a.head_dim == 64) return launch_d<64>(p, stream);
-  return launch_d<128>(p, stream);
+  if (p.a.head_dim == 64) return launch_d<64, false>(p, stream);
+  return launch_d<128, false>(p, stream);
+}
+
+cudaError_t launch_prefix(const PrefixArgs& p, cudaStream_t stream) {
+  if (p.grid <= 0) return cudaSuccess;
+  if (p.a.head_dim == 64) return launch_d<64, true>(p, stream);
+  return launch_d<128, true>(p, stream);
 }
 
 }  // namespace cb

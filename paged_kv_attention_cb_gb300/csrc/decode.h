@@ -25,6 +25,7 @@ struct DecodeCtaStart {
   int kb1;  // one past its last key block
   int t;    // packed query row of the request
   int seq;  // its seq_len
+  int start;  // its first attended position (StepArgs::kv_start)
 };
 
 struct DecodeArgs {

@@ -27,6 +27,9 @@ struct StepArgs {
   int32_t dtype;     // cb_dtype
   int32_t test_expire_wait;  // CB_FLAG_TEST_WAIT_EXPIRY: a consumer's first wait runs out
   int32_t* error_word;
+  // decode rows: first position a request's row attends here (device, per request; nullptr: 0),
+  // the ones before it being attended elsewhere and joined by the merge
+  const int32_t* kv_start = nullptr;
 };
 
 enum KernelId {
@@ -42,7 +45,8 @@ enum KernelId {
   kPortableQ8 = 9,
   kMergeRowsId = 10,
   kDequantPages = 11,
-  kNumKernels = 12
+  kPrefixTc = 12,
+  kNumKernels = 13
 };
 
 void note_launch_begin(KernelId id, cudaStream_t stream);

@@ -50,14 +50,6 @@ WorkspaceLayout layout_of(size_t bytes, const StepArgs& a) {
   return layout((int32_t)r, a.num_q_heads, a.num_kv_heads, a.head_dim);
 }
 
-// First key block (16 keys) a decode query attends, and the number of blocks it attends.
-int kb_lo_host(int seq, int window) { return (window > 0 ? std::max(0, seq - window) : 0) / 16; }
-
-int decode_units_host(int seq, int window) { return (seq - 1) / 16 - kb_lo_host(seq, window) + 1; }
-
-// CTA of the decode partition that owns global key block u (ranges [b U/C, (b+1) U/C)).
-int cta_of_host(long long u, long long U, int C) { return (int)(((u + 1) * C + U - 1) / U) - 1; }
-
 void combine_common(CombineArgs& c, const StepArgs& a, const DecodeArgs& d) {
   c.a = a;
   c.num_ctas = d.num_ctas;
@@ -92,6 +84,19 @@ int sm_count() {
   }
   return cached[dev];
 }
+
+// First key block (16 keys) a decode query attends, and the number of blocks it attends.
+// (start: its first attended position apart from the window, StepArgs::kv_start).
+int kb_lo_host(int seq, int window, int start) {
+  return (window > 0 ? std::max(start, seq - window) : start) / 16;
+}
+
+int decode_units_host(int seq, int window, int start) {
+  return (seq - 1) / 16 - kb_lo_host(seq, window, start) + 1;
+}
+
+// CTA of the decode partition that owns global key block u (ranges [b U/C, (b+1) U/C)).
+int cta_of_host(long long u, long long U, int C) { return (int)(((u + 1) * C + U - 1) / U) - 1; }
 
 size_t workspace_bytes(int32_t num_requests, int32_t num_tokens, int32_t num_q_heads,
                        int32_t num_kv_heads, int32_t head_dim) {
@@ -128,6 +133,53 @@ int prefill_sm_share(long long decode_bytes, double prefill_flops, int n_prefill
   return best_k;
 }
 
+void plan_decode(Plan& plan, const StepArgs& a, const int32_t* h_qsl, const int32_t* h_seq_lens,
+                 const int32_t* h_start, long long U, int C, const ScatterInputs* scatter) {
+  DecodeArgs& d = plan.decode;
+  const bool scatter_first = scatter != nullptr && !plan.fused_scatter;
+  d.a = a;
+  d.total_units = U;
+  // at least kDecodeMinBlocksPerCta key blocks per CTA: a small step split over every
+  // SM spends more on merging its many segments than it gains in streaming
+  d.num_ctas = (int)std::min<long long>(C, (U + kDecodeMinBlocksPerCta - 1) / kDecodeMinBlocksPerCta);
+  d.units_on_device = 0;
+  // each decode row's new K/V is written by the CTA that reads the request's last key
+  // block (the decode kernel is then the step's first)
+  d.fuse_scatter = plan.fused_scatter ? 1 : 0;
+  d.k_new = scatter ? scatter->k_new : nullptr;
+  d.v_new = scatter ? scatter->v_new : nullptr;
+  d.slot_mapping = scatter ? scatter->slot_mapping : nullptr;
+  d.metadata_ready = scatter_first ? 1 : 0;
+  // where each CTA's range [b*U/C, (b+1)*U/C) starts: (request, its first unit)
+  d.has_table = d.num_ctas <= kDecodeTableCtas;
+  if (d.has_table) {
+    long long u = 0;
+    int b = 0;
+    const long long Cn = d.num_ctas;
+    for (int r = 0; r < a.num_requests && b < d.num_ctas; ++r) {
+      const int ql = h_qsl[r + 1] - h_qsl[r];
+      if (ql != 1 || h_seq_lens[r] <= 0) continue;
+      const int start = h_start ? h_start[r] : 0;
+      const int units = decode_units_host(h_seq_lens[r], a.sliding_window, start);
+      const int kbl = kb_lo_host(h_seq_lens[r], a.sliding_window, start);
+      while (b < d.num_ctas && (long long)b * U / Cn < u + units) {
+        const long long lo = (long long)b * U / Cn, hi = (long long)(b + 1) * U / Cn;
+        d.cta_first[b] = DecodeCtaStart{r, (int)u, kbl + (int)(lo - u),
+                                        kbl + (int)(std::min(u + units, hi) - u), h_qsl[r],
+                                        h_seq_lens[r], start};
+        ++b;
+      }
+      u += units;
+    }
+    for (; b < d.num_ctas; ++b) d.cta_first[b] = DecodeCtaStart{-1, 0, 0, 0, 0, 0, 0};
+  }
+  const WorkspaceLayout w = layout_of(plan.workspace_bytes, a);
+  uint8_t* ws = static_cast<uint8_t*>(plan.workspace);
+  d.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
+  d.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  plan.decode_plan.smem_bytes = decode_smem_bytes(d.stages, d.stage_bytes, d.q_slot_bytes);
+}
+
 void plan_step(Plan& plan, const StepArgs& a, const int32_t* h_qsl, const int32_t* h_seq_lens,
                uint32_t flags, const ScatterInputs* scatter, void* workspace,
                size_t workspace_bytes) {
@@ -149,7 +201,7 @@ void plan_step(Plan& plan, const StepArgs& a, const int32_t* h_qsl, const int32_
   for (int r = 0; r < a.num_requests; ++r) {
     const int ql = h_qsl[r + 1] - h_qsl[r];
     if (ql == 1 && h_seq_lens[r] > 0) {
-      U += decode_units_host(h_seq_lens[r], a.sliding_window);
+      U += decode_units_host(h_seq_lens[r], a.sliding_window, 0);
     } else if (ql > 1) {
       has_prefill = true;
       const long long ctx = h_seq_lens[r] - ql;
@@ -188,6 +240,7 @@ void plan_step(Plan& plan, const StepArgs& a, const int32_t* h_qsl, const int32_
     const size_t fixed = decode_smem_bytes(0, d.stage_bytes, d.q_slot_bytes);
     d.stages = (int)std::min<size_t>(kDecodeMaxStages, (kDecodeSmemLimit - fixed) / d.stage_bytes);
     plan.fast_decode = d.stages >= 2;
+    d.heads_per_cta = HB;
   }
   plan.fast_prefill = prefill_ok;
   if (plan.fast_decode && plan.fast_prefill) plan.portable_mode = -1;
@@ -245,52 +298,12 @@ void plan_step(Plan& plan, const StepArgs& a, const int32_t* h_qsl, const int32_
 
   // ---- decode rows: split-KV kernel
   if (plan.fast_decode) {
-    d.a = a;
-    d.heads_per_cta = HB;
-    d.total_units = U;
     int C = std::min(sm_count(), kMaxDecodeCtas);
     if (plan.concurrent) {
       const long long bytes = U * 16LL * 2 * a.num_kv_heads * a.head_dim * 2;
       C = sm_count() - prefill_sm_share(bytes, flops, prefill_total_ctas, sm_count());
     }
-    // at least kDecodeMinBlocksPerCta key blocks per CTA: a small step split over every
-    // SM spends more on merging its many segments than it gains in streaming
-    d.num_ctas = (int)std::min<long long>(C, (U + kDecodeMinBlocksPerCta - 1) / kDecodeMinBlocksPerCta);
-    d.units_on_device = 0;
-    // each decode row's new K/V is written by the CTA that reads the request's last key
-    // block (the decode kernel is then the step's first)
-    d.fuse_scatter = plan.fused_scatter ? 1 : 0;
-    d.k_new = scatter ? scatter->k_new : nullptr;
-    d.v_new = scatter ? scatter->v_new : nullptr;
-    d.slot_mapping = scatter ? scatter->slot_mapping : nullptr;
-    d.metadata_ready = scatter_first ? 1 : 0;
-    // where each CTA's range [b*U/C, (b+1)*U/C) starts: (request, its first unit)
-    d.has_table = d.num_ctas <= kDecodeTableCtas;
-    if (d.has_table) {
-      long long u = 0;
-      int b = 0;
-      const long long Cn = d.num_ctas;
-      for (int r = 0; r < a.num_requests && b < d.num_ctas; ++r) {
-        const int ql = h_qsl[r + 1] - h_qsl[r];
-        if (ql != 1 || h_seq_lens[r] <= 0) continue;
-        const int units = decode_units_host(h_seq_lens[r], a.sliding_window);
-        const int kbl = kb_lo_host(h_seq_lens[r], a.sliding_window);
-        while (b < d.num_ctas && (long long)b * U / Cn < u + units) {
-          const long long lo = (long long)b * U / Cn, hi = (long long)(b + 1) * U / Cn;
-          d.cta_first[b] = DecodeCtaStart{r, (int)u, kbl + (int)(lo - u),
-                                          kbl + (int)(std::min(u + units, hi) - u), h_qsl[r],
-                                          h_seq_lens[r]};
-          ++b;
-        }
-        u += units;
-      }
-      for (; b < d.num_ctas; ++b) d.cta_first[b] = DecodeCtaStart{-1, 0, 0, 0, 0, 0};
-    }
-    const WorkspaceLayout w = layout_of(workspace_bytes, a);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    d.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
-    d.part_o = reinterpret_cast<float*>(ws + w.part_o);
-    plan.decode_plan.smem_bytes = decode_smem_bytes(d.stages, d.stage_bytes, d.q_slot_bytes);
+    plan_decode(plan, a, h_qsl, h_seq_lens, nullptr, U, C, scatter);
     // the requests split over several CTAs, merged by the combine launch
     CombineArgs& c = plan.combine;
     combine_common(c, a, d);
@@ -299,7 +312,7 @@ void plan_step(Plan& plan, const StepArgs& a, const int32_t* h_qsl, const int32_
     for (int r = 0; r < a.num_requests; ++r) {
       const int ql = h_qsl[r + 1] - h_qsl[r];
       if (ql != 1 || h_seq_lens[r] <= 0) continue;
-      const int units = decode_units_host(h_seq_lens[r], a.sliding_window);
+      const int units = decode_units_host(h_seq_lens[r], a.sliding_window, 0);
       const int b0 = cta_of_host(u, U, d.num_ctas);
       const int b1 = cta_of_host(u + units - 1, U, d.num_ctas);
       u += units;

@@ -49,6 +49,17 @@ struct Plan {
 
 // scatter: the step's new rows (nullptr: none). Unless the plan fuses them into the
 // decode kernel (fused_scatter), the caller launches the scatter before run_plan.
+// Key blocks (16 keys) a decode row attends (start: StepArgs::kv_start), and the CTA of C that
+// owns key block u of U.
+int decode_units_host(int seq, int window, int start);
+int cta_of_host(long long u, long long U, int C);
+
+// The decode launch of a plan whose kernel choice (fast_decode, fused_scatter, stages) is made,
+// over C CTAs at most. h_start: host copy of a.kv_start (nullptr: all 0); U: the key blocks of
+// all decode rows.
+void plan_decode(Plan& plan, const StepArgs& a, const int32_t* h_qsl, const int32_t* h_seq_lens,
+                 const int32_t* h_start, long long U, int C, const ScatterInputs* scatter);
+
 void plan_step(Plan& plan, const StepArgs& a, const int32_t* h_qsl, const int32_t* h_seq_lens,
                uint32_t flags, const ScatterInputs* scatter, void* workspace,
                size_t workspace_bytes);

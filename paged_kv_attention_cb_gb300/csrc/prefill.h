@@ -56,6 +56,25 @@ struct PrefillArgs {
   PrefillEntry entries[kPrefillMaxEntries];  // heaviest first
 };
 
+// The same tiles over a prefix that the requests of a group share: an entry is a group, its
+// "request" r any of the group's (they have the same leading pages), its query tokens the group's
+// packed decode rows, seq_len the prefix's length; every row attends all of it. The key tiles are
+// split into units of tiles_per_unit, whose results are partial rows for the merge: token i of
+// entry e in split s is row part_row[e] + s * q_len + i.
+struct PrefixArgs : PrefillArgs {
+  int tiles_per_unit;
+  int part_row[kPrefillMaxEntries];
+  float* part_o;    // [row][Hq][D] unnormalised
+  float2* part_ml;  // [row][Hq] (running maximum in log2 units, sum)
+};
+
+// Key tiles of a prefix, and the units they are split into.
+inline int prefix_key_tiles(int seq_len) { return (seq_len + 127) / 128; }
+inline int prefix_splits(int seq_len, int tiles_per_unit) {
+  return (prefix_key_tiles(seq_len) + tiles_per_unit - 1) / tiles_per_unit;
+}
+cudaError_t launch_prefix(const PrefixArgs& p, cudaStream_t stream);
+
 size_t prefill_smem_bytes(int head_dim);
 // Most prefill CTAs a step of up to `num_tokens` query tokens in `num_requests`
 // requests can need (the grid of a launch whose work is found on the device).

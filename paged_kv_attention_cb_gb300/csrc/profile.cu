@@ -42,7 +42,8 @@ cudaEvent_t take_event() {
 const char* const kNames[kNumKernels] = {"write_kv", "portable_attention", "decode_split",
                                          "prefill_tc", "copy_blocks", "decode_combine",
                                          "write_kv_q8", "read_kv_q8", "decode_q8",
-                                         "portable_q8", "merge_rows", "dequant_pages"};
+                                         "portable_q8", "merge_rows", "dequant_pages",
+                                         "prefix_tc"};
 
 }  // namespace
 
