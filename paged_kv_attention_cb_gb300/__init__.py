@@ -345,88 +345,153 @@ def no_alloc_read_error_word(stream=None) -> int:
     return int(word.value)
 
 
+# ------------------------------------------------- checked calls (8-bit cache, shared prefixes)
+#
+# These entry points check every tensor (type, shape, contiguity, device) before the call. The
+# checks run on whole lists at once: a small decode step takes ~10 us on the GPU, and a Python
+# statement per tensor and property took longer than that.
+
+
+class _Torch:
+    """torch's types and methods that the checks use, looked up on first use (the module itself
+    imports without torch)."""
+
+    def __init__(self):
+        import torch
+
+        self.e4m3 = (torch.float8_e4m3fn, torch.uint8)
+        self.e8m0 = (torch.float8_e8m0fnu, torch.uint8)
+        self.i32, self.i64 = torch.int32, torch.int64
+        self.code = {torch.float32: CB_F32, torch.bfloat16: CB_BF16}
+        self.device_of = torch.Tensor.get_device
+        self.contiguous = torch.Tensor.is_contiguous
+        self.ptr = torch.Tensor.data_ptr
+        self.current_device = torch.cuda.current_device
+        self.device = torch.cuda.device
+        # the raw handle of the current stream; the public call wraps it in an object first
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
+_TORCH = None
+_NP_I32 = np.dtype(np.int32)
+_addressof, _from_buffer = ctypes.addressof, ctypes.c_char.from_buffer
+
+
+def _torch() -> _Torch:
+    global _TORCH
+    if _TORCH is None:
+        _TORCH = _Torch()
+    return _TORCH
+
+
+def _pointers(tensors, shapes, dtypes, names):
+    """The data pointers of contiguous tensors of these shapes and dtypes, all on one CUDA device,
+    and its index. ``names``: a function that gives their names, for the error."""
+    t = _torch()
+    device = t.device_of(tensors[0])
+    if (device >= 0 and tuple([x.shape for x in tensors]) == shapes
+            and tuple([x.dtype for x in tensors]) == dtypes and all(map(t.contiguous, tensors))
+            and set(map(t.device_of, tensors)) == {device}):
+        return list(map(t.ptr, tensors)), device
+    names = names()
+    for x, name, shape, dtype in zip(tensors, names, shapes, dtypes):
+        if x.dtype != dtype:
+            raise CbError(1, f"{name}: dtype {x.dtype}, not {dtype}")
+        if tuple(x.shape) != tuple(shape):
+            raise CbError(1, f"{name}: shape {tuple(x.shape)}, not {tuple(shape)}")
+        if not x.is_contiguous():
+            raise CbError(1, f"{name} must be contiguous")
+        if not x.is_cuda or x.device != tensors[0].device:
+            raise CbError(1, f"{name} must be on the CUDA device of {names[0]}")
+    raise CbError(1, "tensors must be on a CUDA device")
+
+
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) with the tensors' device current: the library launches on it."""
+    t = _torch()
+    if stream is None:
+        stream = t.stream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if device == t.current_device():
+        status = fn(*args, stream)
+    else:
+        with t.device(device):
+            status = fn(*args, stream)
+    if status:
+        _check(status)
+
+
+def _mirror(a, n, name):
+    """A host mirror as a contiguous int32 array of n entries, and its address (ndarray.ctypes takes
+    a microsecond; the buffer protocol a third of it, for writable arrays)."""
+    if type(a) is not np.ndarray or a.dtype != _NP_I32 or not a.flags.c_contiguous:
+        a = _host_i32(a)
+    if a.shape != (n,):
+        raise CbError(2, f"{name}: {a.shape} entries, not {n}")
+    if a.flags.writeable and n:
+        return a, _addressof(_from_buffer(a))
+    return a, a.ctypes.data
+
+
+def _dims(t, n, name):
+    if t.dim() != n:
+        raise CbError(1, f"{name}: {t.dim()} dimensions, not {n}")
+    return t.shape
+
+
+def _float_type(t, name):
+    code = _torch().code.get(t.dtype)
+    if code is None:
+        raise CbError(1, f"{name}: dtype {t.dtype}, not torch.float32 or torch.bfloat16")
+    return code
+
+
 # ---------------------------------------------------------------- 8-bit paged cache
 
 
-def _need(t, name, shape, kinds, device=None):
-    """A contiguous CUDA tensor of the given shape and one of the given dtypes."""
-    if t.dtype not in kinds:
-        raise CbError(1, f"{name}: dtype {t.dtype}, not one of {', '.join(map(str, kinds))}")
-    if t.shape != shape:
-        raise CbError(1, f"{name}: shape {tuple(t.shape)}, not {tuple(shape)}")
-    if not t.is_contiguous():
-        raise CbError(1, f"{name} must be contiguous")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise CbError(1, f"{name} must be on {'a CUDA device' if device is None else device}")
+_CACHE_NAMES = ("k_cache", "v_cache", "k_scale", "v_scale")
 
 
-def _kinds():
-    global _E4M3, _E8M0, _I32, _I64, _FLOATS
-    import torch
-
-    _E4M3 = (torch.float8_e4m3fn, torch.uint8)
-    _E8M0 = (torch.float8_e8m0fnu, torch.uint8)
-    _I32 = (torch.int32,)
-    _I64 = (torch.int64,)
-    _FLOATS = (torch.bfloat16, torch.float32)
-
-
-_E4M3 = _E8M0 = _I32 = _I64 = _FLOATS = None
-
-
-def _need_cache_q8(k_cache, v_cache, k_scale, v_scale, Hkv, D, device):
-    """Checks the four arrays of an 8-bit cache; returns (num_blocks, block_size)."""
-    shape = k_cache.shape
-    if len(shape) != 4 or shape[2] != Hkv or shape[3] != D:
-        raise CbError(1, f"k_cache: shape {tuple(shape)}, not [num_blocks, block_size, {Hkv}, {D}]")
-    _need(k_cache, "k_cache", shape, _E4M3, device)
-    _need(v_cache, "v_cache", shape, _E4M3, device)
-    _need(k_scale, "k_scale", shape[:3], _E8M0, device)
-    _need(v_scale, "v_scale", shape[:3], _E8M0, device)
-    return shape[0], shape[1]
+def _cache_q8(k_cache, v_cache, k_scale, v_scale):
+    """(tensors, shapes, dtypes) of an 8-bit cache."""
+    t = _torch()
+    shape = _dims(k_cache, 4, "k_cache")
+    value, scale = k_cache.dtype, k_scale.dtype
+    if value not in t.e4m3:
+        raise CbError(1, f"k_cache: dtype {value}, not {' or '.join(map(str, t.e4m3))}")
+    if scale not in t.e8m0:
+        raise CbError(1, f"k_scale: dtype {scale}, not {' or '.join(map(str, t.e8m0))}")
+    rows = shape[:3]
+    return ((k_cache, v_cache, k_scale, v_scale), (shape, shape, rows, rows),
+            (value, value, scale, scale))
 
 
-def _on(device):
-    """The guard under which a call for tensors on ``device`` runs: the library launches on the
-    current device."""
-    import contextlib
-
-    import torch
-
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
-
-
-def _stream_on(stream, device):
-    if stream is not None:
-        return _stream(stream)
-    import torch
-
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
-def _rows_q8(fn, a, b, rows, cache, slot_mapping, error_word, stream):
-    if _E4M3 is None:
-        _kinds()
-    k = rows[0]
-    if k.dim() != 3:
-        raise CbError(1, f"rows must be [T, Hkv, D], not {tuple(k.shape)}")
-    T, Hkv, D = k.shape
-    dev = k.device
-    _need(rows[0], a, k.shape, _FLOATS)
-    _need(rows[1], b, k.shape, (k.dtype,), dev)
-    NB, BS = _need_cache_q8(*cache, Hkv, D, dev)
-    _need(slot_mapping, "slot_mapping", (T,), _I64, dev)
+def _rows_q8(fn, rows, names, cache, slot_mapping, error_word, stream):
+    t = _torch()
+    a, b = rows
+    code = _float_type(a, names[0])
+    shape = T, Hkv, D = _dims(a, 3, names[0])
+    tensors, shapes, dtypes = _cache_q8(*cache)
+    NB, BS, H, Dc = shapes[0]
+    if H != Hkv or Dc != D:
+        raise CbError(1, f"k_cache: rows of {(H, Dc)}, not {(Hkv, D)}")
+    kind = a.dtype
+    tensors = (a, b, *tensors, slot_mapping)
+    shapes = (shape, shape, *shapes, (T,))
+    dtypes = (kind, kind, *dtypes, t.i64)
     if error_word is not None:
-        _need(error_word, "error_word", error_word.shape, _I32, dev)
-    c = [t.data_ptr() for t in cache]
-    r = [t.data_ptr() for t in rows]
-    ptrs = (*r, *c, slot_mapping.data_ptr()) if fn == "cb_write_kv_q8" else (
-        *c, slot_mapping.data_ptr(), *r)
-    with _on(dev):
-        _check(getattr(lib(), fn)(*ptrs, T, NB, BS, Hkv, D, _dtype_code(k), _ptr(error_word),
-                                  _stream_on(stream, dev)))
+        tensors, shapes, dtypes = (*tensors, error_word), (*shapes, error_word.shape), (*dtypes, t.i32)
+    p, device = _pointers(tensors, shapes, dtypes,
+                          lambda: (*names, *_CACHE_NAMES, "slot_mapping", "error_word"))
+    word = p[7] if error_word is not None else None
+    if names[0] == "k_out":
+        _call(fn, device, stream, p[2], p[3], p[4], p[5], p[6], p[0], p[1], T, NB, BS, Hkv, D,
+              code, word)
+    else:
+        _call(fn, device, stream, p[0], p[1], p[2], p[3], p[4], p[5], p[6], T, NB, BS, Hkv, D,
+              code, word)
 
 
 def write_kv_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping, error_word=None,
@@ -434,7 +499,7 @@ def write_kv_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping, 
     """Quantise k_new/v_new [T, Hkv, D] (bf16 or fp32) into the 8-bit caches [NB, BS, Hkv, D]
     (float8_e4m3fn) and their scales [NB, BS, Hkv] (float8_e8m0fnu) at slot_mapping [T].
     uint8 tensors are taken for either as well (see cb_write_kv_q8 in include/cb.h)."""
-    _rows_q8("cb_write_kv_q8", "k_new", "v_new", (k_new, v_new),
+    _rows_q8(lib().cb_write_kv_q8, (k_new, v_new), ("k_new", "v_new"),
              (k_cache, v_cache, k_scale, v_scale), slot_mapping, error_word, stream)
 
 
@@ -442,7 +507,7 @@ def read_kv_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out, e
                stream=None):
     """k_out/v_out [T, Hkv, D] (bf16 or fp32) = the 8-bit caches' rows at slot_mapping [T]
     (rows of negative slots stay as they are; see cb_read_kv_q8 in include/cb.h)."""
-    _rows_q8("cb_read_kv_q8", "k_out", "v_out", (k_out, v_out),
+    _rows_q8(lib().cb_read_kv_q8, (k_out, v_out), ("k_out", "v_out"),
              (k_cache, v_cache, k_scale, v_scale), slot_mapping, error_word, stream)
 
 
@@ -462,37 +527,43 @@ def alloc_workspace_q8(num_requests, num_tokens, num_q_heads, num_kv_heads, head
     return torch.zeros((n + 15) // 16 * 16, dtype=torch.uint8, device=device)
 
 
-def _step_checks(out, q, Hkv, query_start_loc, seq_lens, block_table, h_query_start_loc,
-                 h_seq_lens, k_new, v_new, slot_mapping, workspace):
-    """The tensors every step takes; returns (T, Hq, D, R, stride, host mirrors, device)."""
-    if _E4M3 is None:
-        _kinds()
-    if q.dim() != 3:
-        raise CbError(1, f"q must be [T, Hq, D], not {tuple(q.shape)}")
-    T, Hq, D = q.shape
-    dev = q.device
-    _need(q, "q", q.shape, _FLOATS)
-    kinds = (q.dtype,)
-    _need(out, "out", q.shape, kinds, dev)
-    R = seq_lens.shape[0]
-    _need(seq_lens, "seq_lens", (R,), _I32, dev)
-    _need(query_start_loc, "query_start_loc", (R + 1,), _I32, dev)
-    if block_table.dim() != 2:
-        raise CbError(1, "block_table must be [R, stride]")
-    stride = block_table.shape[1]
-    _need(block_table, "block_table", (R, stride), _I32, dev)
+_STEP_NAMES = ("q", "out", "query_start_loc", "seq_lens", "block_table", "workspace")
+_NEW_NAMES = ("k_new", "v_new", "slot_mapping")
+
+
+def _step(out, q, query_start_loc, seq_lens, block_table, workspace, cache, cache_names, k_new,
+          v_new, slot_mapping):
+    """Checks the tensors of a step over `cache` (tensors, shapes, dtypes; the first one the K
+    cache). Returns the pointers -- q, out, query_start_loc, seq_lens, block_table, workspace,
+    cache..., k_new, v_new, slot_mapping -- the device, and the sizes."""
+    t = _torch()
+    code = _float_type(q, "q")
+    qs = T, Hq, D = _dims(q, 3, "q")
+    (R,) = rs = _dims(seq_lens, 1, "seq_lens")
+    stride = _dims(block_table, 2, "block_table")[1]
+    ctensors, cshapes, cdtypes = cache
+    NB, BS, Hkv, Dc = cshapes[0]
+    if Dc != D:
+        raise CbError(1, f"k_cache: head_dim {Dc}, not {D}")
+    i32, kind = t.i32, q.dtype
     if k_new is not None:
         if v_new is None or slot_mapping is None:
             raise CbError(1, "k_new given without v_new or slot_mapping")
-        _need(k_new, "k_new", (T, Hkv, D), kinds, dev)
-        _need(v_new, "v_new", (T, Hkv, D), kinds, dev)
-        _need(slot_mapping, "slot_mapping", (T,), _I64, dev)
-    if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
-        raise CbError(4, f"workspace must be contiguous, on {dev}")
-    hq, hs = _host_i32(h_query_start_loc), _host_i32(h_seq_lens)
-    if hq.shape != (R + 1,) or hs.shape != (R,):
-        raise CbError(2, "host mirrors must have R+1 and R entries")
-    return T, Hq, D, R, stride, hq, hs, dev
+        rows = (T, Hkv, D)
+        p, device = _pointers(
+            (q, out, query_start_loc, seq_lens, block_table, workspace, *ctensors, k_new, v_new,
+             slot_mapping),
+            (qs, qs, (R + 1,), rs, (R, stride), workspace.shape, *cshapes, rows, rows, (T,)),
+            (kind, kind, i32, i32, i32, workspace.dtype, *cdtypes, kind, kind, t.i64),
+            lambda: (*_STEP_NAMES, *cache_names, *_NEW_NAMES))
+    else:
+        p, device = _pointers(
+            (q, out, query_start_loc, seq_lens, block_table, workspace, *ctensors),
+            (qs, qs, (R + 1,), rs, (R, stride), workspace.shape, *cshapes),
+            (kind, kind, i32, i32, i32, workspace.dtype, *cdtypes),
+            lambda: (*_STEP_NAMES, *cache_names))
+        p += (None, None, None)
+    return p, device, code, T, Hq, D, R, stride, NB, BS, Hkv
 
 
 def paged_attention_q8(out, q, k_cache, v_cache, k_scale, v_scale, query_start_loc, seq_lens,
@@ -505,20 +576,15 @@ def paged_attention_q8(out, q, k_cache, v_cache, k_scale, v_scale, query_start_l
     [NB, BS, Hkv] float8_e8m0fnu (or uint8); the step's k_new/v_new are quantised into their
     slots first. workspace: alloc_workspace_q8.
     """
-    Hkv = k_cache.shape[2] if k_cache.dim() == 4 else 0
-    T, Hq, D, R, stride, hq, hs, dev = _step_checks(
-        out, q, Hkv, query_start_loc, seq_lens, block_table, h_query_start_loc, h_seq_lens, k_new,
-        v_new, slot_mapping, workspace)
-    NB, BS = _need_cache_q8(k_cache, v_cache, k_scale, v_scale, Hkv, D, dev)
-    with _on(dev):
-        _check(lib().cb_paged_attention_q8(
-            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            k_scale.data_ptr(), v_scale.data_ptr(), _ptr(k_new),
-            _ptr(v_new), _ptr(slot_mapping),
-            query_start_loc.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), stride,
-            hq.ctypes.data, hs.ctypes.data, R, T, NB, BS, Hq, Hkv, D, float(scale),
-            int(sliding_window), _dtype_code(q), int(flags), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), _stream_on(stream, dev)))
+    p, device, dtype, T, Hq, D, R, stride, NB, BS, Hkv = _step(
+        out, q, query_start_loc, seq_lens, block_table, workspace,
+        _cache_q8(k_cache, v_cache, k_scale, v_scale), _CACHE_NAMES, k_new, v_new, slot_mapping)
+    hq, hq_at = _mirror(h_query_start_loc, R + 1, "h_query_start_loc")
+    hs, hs_at = _mirror(h_seq_lens, R, "h_seq_lens")
+    pq, pout, pqsl, pseq, pbt, pws, pk, pv, pks, pvs, pkn, pvn, psl = p
+    _call(lib().cb_paged_attention_q8, device, stream, pout, pq, pk, pv, pks, pvs, pkn, pvn, psl,
+          pqsl, pseq, pbt, stride, hq_at, hs_at, R, T, NB, BS, Hq, Hkv, D, scale, sliding_window,
+          dtype, flags, pws, workspace.numel() * workspace.element_size())
     return out
 
 
@@ -550,29 +616,23 @@ def paged_attention_shared(out, q, k_cache, v_cache, query_start_loc, seq_lens, 
     shares with its group; h_group_start [n_groups + 1] on the host: group g is the requests
     h_group_start[g] .. h_group_start[g + 1] - 1. workspace: alloc_workspace_shared.
     """
-    Hkv = k_cache.shape[2] if k_cache.dim() == 4 else 0
-    T, Hq, D, R, stride, hq, hs, dev = _step_checks(
-        out, q, Hkv, query_start_loc, seq_lens, block_table, h_query_start_loc, h_seq_lens, k_new,
-        v_new, slot_mapping, workspace)
-    shape = k_cache.shape
-    if len(shape) != 4 or shape[3] != D:
-        raise CbError(1, f"k_cache: shape {tuple(shape)}, not [num_blocks, block_size, Hkv, {D}]")
-    kinds = (q.dtype,)
-    _need(k_cache, "k_cache", shape, kinds, dev)
-    _need(v_cache, "v_cache", shape, kinds, dev)
-    _need(prefix_lens, "prefix_lens", (R,), _I32, dev)
-    hp, hg = _host_i32(h_prefix_lens), _host_i32(h_group_start)
-    if hp.shape != (R,) or hg.ndim != 1 or not len(hg):
-        raise CbError(2, "h_prefix_lens must have R entries, h_group_start n_groups + 1")
-    with _on(dev):
-        _check(lib().cb_paged_attention_shared(
-            out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_new),
-            _ptr(v_new), _ptr(slot_mapping), query_start_loc.data_ptr(), seq_lens.data_ptr(),
-            block_table.data_ptr(), stride, prefix_lens.data_ptr(), hq.ctypes.data,
-            hs.ctypes.data, hp.ctypes.data, hg.ctypes.data, len(hg) - 1, R, T, shape[0], shape[1],
-            Hq, Hkv, D, float(scale), int(sliding_window), _dtype_code(q), int(flags),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-            _stream_on(stream, dev)))
+    shape = _dims(k_cache, 4, "k_cache")
+    cache = ((k_cache, v_cache, prefix_lens), (shape, shape, seq_lens.shape),
+             (q.dtype, q.dtype, _torch().i32))
+    p, device, dtype, T, Hq, D, R, stride, NB, BS, Hkv = _step(
+        out, q, query_start_loc, seq_lens, block_table, workspace, cache,
+        ("k_cache", "v_cache", "prefix_lens"), k_new, v_new, slot_mapping)
+    groups = len(h_group_start) - 1
+    if groups < 0:
+        raise CbError(2, "h_group_start must have n_groups + 1 entries")
+    hq, hq_at = _mirror(h_query_start_loc, R + 1, "h_query_start_loc")
+    hs, hs_at = _mirror(h_seq_lens, R, "h_seq_lens")
+    hp, hp_at = _mirror(h_prefix_lens, R, "h_prefix_lens")
+    hg, hg_at = _mirror(h_group_start, groups + 1, "h_group_start")
+    pq, pout, pqsl, pseq, pbt, pws, pk, pv, ppl, pkn, pvn, psl = p
+    _call(lib().cb_paged_attention_shared, device, stream, pout, pq, pk, pv, pkn, pvn, psl, pqsl,
+          pseq, pbt, stride, ppl, hq_at, hs_at, hp_at, hg_at, groups, R, T, NB, BS, Hq, Hkv, D,
+          scale, sliding_window, dtype, flags, pws, workspace.numel() * workspace.element_size())
     return out
 
 

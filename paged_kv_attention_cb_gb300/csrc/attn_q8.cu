@@ -58,9 +58,10 @@ constexpr int kKB = kQ8KeyBlock;
 constexpr float kNoMax = -1e30f;     // running maximum before any key (finite: no inf - inf)
 constexpr float kRaise = 8.f;        // the maxima are raised when exceeded by more than 2^8
 constexpr float kWeightLog2 = 6.f;   // weights are at most 2^(8 + 6), inside fp16's range
-constexpr int kMaxQueue = 2;         // pieces handed ahead to the consumers
+constexpr int kQueue = 4;            // pieces handed ahead to the consumers
 
 struct Q8Piece {
+  int r;       // request
   int t0;      // packed query row of the item's first token (-1: no more pieces)
   int ntok;
   int n;       // key blocks of this piece
@@ -68,16 +69,26 @@ struct Q8Piece {
   int pos0;    // position of the first token
   int slot;    // partial slot: 2 b for CTA b's first piece, 2 b + 1 for its last
   int direct;  // the whole item lies in this CTA
+  int last;    // the piece ends with the item's last key block
+};
+
+// The new row of the request whose last block a consumer warp is going to read, quantised.
+struct Q8NewRow {
+  uint32_t k[32], v[32];  // D / 4 words each
+  int k_code, v_code;
+  long long row;          // its row in the cache (slot * Hkv + head), -1: not written
+  int staged;             // its slot is its own position's: it is attended as well
 };
 
 struct Q8Smem {
   uint64_t full[kQ8MaxStages];
   uint64_t empty[kQ8MaxStages];
-  uint64_t pfull[kMaxQueue];
-  uint64_t pempty[kMaxQueue];
+  uint64_t pfull[kQueue];
+  uint64_t pempty[kQueue];
   uint64_t xfull[16];   // exchange slot written by warp (key warp, head)
   uint64_t xempty[16];  // and read
-  Q8Piece piece[kMaxQueue];
+  Q8Piece piece[kQueue];
+  Q8NewRow fresh[16];  // by consumer warp: the warps of a head may be pieces apart
   int abort_flag;
 };
 
@@ -120,6 +131,23 @@ CB_DEV uint32_t pack_f16x2_rest(uint32_t rounded, float lo, float hi) {
 CB_DEV uint32_t f16x2_lo(uint32_t w) { return f16x2_of_e4m3x2((uint16_t)w); }
 CB_DEV uint32_t f16x2_hi(uint32_t w) { return f16x2_of_e4m3x2((uint16_t)(w >> 16)); }
 
+// Ask for the line of `p` in L1 (a hint).
+CB_DEV void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
+// A operand of O^T = V^T P^T for two output tiles of head_dim: words of four V rows (keys 2t, 2t+1,
+// 2t+8, 2t+9), the bytes of a pair of keys side by side (bytes 0, 1 of the words, or 2, 3).
+CB_DEV void v_fragment(uint32_t (&a)[4], uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3, bool hi) {
+  const uint32_t sel = hi ? 0x7362u : 0x5140u;
+  const uint32_t x = __byte_perm(v0, v1, sel), y = __byte_perm(v2, v3, sel);
+  a[0] = f16x2_lo(x);
+  a[1] = f16x2_hi(x);
+  a[2] = f16x2_lo(y);
+  a[3] = f16x2_hi(y);
+}
+
+// 0xff in the bytes that are e4m3 NaNs, else 0.
+CB_DEV uint32_t nan_bytes(uint32_t x) { return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
 CB_DEV uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -140,15 +168,43 @@ CB_DEV int lds_u8(uint32_t addr) {
   return (int)v;
 }
 
+CB_DEV void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+CB_DEV void sts8(uint32_t addr, int v) {
+  asm volatile("st.shared.b8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// Four values of a row (16-byte aligned fp32, 8-byte aligned bf16), their largest finite
+// magnitude's bits, and their e4m3 bytes.
+template <bool F32>
+CB_DEV void load4(const void* rows, long long at, float (&x)[4]) {
+  if constexpr (F32) {
+    const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(rows) + at));
+    x[0] = v.x;
+    x[1] = v.y;
+    x[2] = v.z;
+    x[3] = v.w;
+  } else {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(rows) + at));
+    x[0] = __uint_as_float(v.x << 16);
+    x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16);
+    x[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+}
+CB_DEV uint32_t magnitude4(const float (&x)[4]) {
+  return max(max(finite_magnitude(x[0]), finite_magnitude(x[1])),
+             max(finite_magnitude(x[2]), finite_magnitude(x[3])));
+}
+CB_DEV uint32_t quantise4(const float (&x)[4], float inv) {
+  return e4m3x2_of(x[0] * inv, x[1] * inv) | (e4m3x2_of(x[2] * inv, x[3] * inv) << 16);
+}
+
 // First key block of a run of ntok tokens starting at position pos0, and how many it attends.
 CB_DEV int first_key(int pos0, int window) { return window > 0 ? max(0, pos0 - window + 1) : 0; }
 CB_DEV int blocks_of(int pos0, int ntok, int window) {
   return (pos0 + ntok - 1) / kKB - first_key(pos0, window) / kKB + 1;
-}
-
-// CTA that owns global block u (ranges [b U / C, (b + 1) U / C)).
-CB_DEV int owner_of(long long u, long long U, int C) {
-  return (int)(((u + 1) * (long long)C + U - 1) / U) - 1;
 }
 
 }  // namespace
@@ -160,7 +216,6 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ Q8Args p) {
   constexpr int kKS = D / 16;          // contraction steps over head_dim; output tiles of 16
   constexpr int kSplit = F32 ? 2 : 1;  // fp16 parts of q and of the weights
-  constexpr int kXRegs = 16;           // outputs per exchange round
   extern __shared__ __align__(1024) uint8_t smem_dyn[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
@@ -171,7 +226,8 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
   uint8_t* stages = base;
   uint8_t* scales = stages + p.stages * stage_bytes;
   float* xchg = reinterpret_cast<float*>(scales + p.stages * 2 * scale_bytes);
-  constexpr int kXFloats = (6 * NB + kXRegs) * 32;
+  constexpr int kORegs = NB * kKS * 4;      // outputs of a lane
+  constexpr int kXFloats = (6 * NB + kORegs) * 32;
   Q8Smem& sm = *reinterpret_cast<Q8Smem*>(xchg + (KW - 1) * HB * kXFloats);
 
   const int warp = threadIdx.x >> 5;
@@ -181,15 +237,13 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
   const int nwarps = HB * KW;  // consumer warps; the next one is the producer
   const int W = p.a.sliding_window;
   const int TT = p.tile_tokens;
-  const long long U = p.total_units;
-  const int C = p.num_ctas;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], HB);
     }
-    for (int s = 0; s < kMaxQueue; ++s) {
+    for (int s = 0; s < kQueue; ++s) {
       mbar_init(&sm.pfull[s], 1);
       mbar_init(&sm.pempty[s], nwarps);
     }
@@ -215,13 +269,13 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
   int issued_blocks = 0;  // producer: copies issued (for the drain)
   if (warp == nwarps) {
     // =================================================== producer warp
-    const long long u_lo = (long long)b * U / C;
-    const long long u_hi = (long long)(b + 1) * U / C;
+    const int u_lo = p.start[b].u, u_hi = p.start[b + 1].u;
     const uint64_t policy = l2_policy_evict_first();  // the stream is read once
     const int BS = p.a.block_size;
     bool ok = true;
     int k = 0;  // pieces handed out
     int i = 0;  // blocks issued
+    int s = 0, round = 0;  // i % stages, i / stages
     // Request metadata, 32 requests at a time (lane l: request wbase + l).
     int wbase = -1, w_t = 0, w_q = 0, w_seq = 0;
     auto load_window = [&](int r0) {
@@ -246,7 +300,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
     };
     // the current item: its request's fields, its first block and its block count
     int r = p.start[b].r, tile = p.start[b].tile;
-    long long u0 = p.start[b].u0;
+    int u0 = p.start[b].u0;
     int t0 = 0, qlen = 0, seq = 0, pos0 = 0, ntok = 0, nblk = 0, kb_lo = 0;
     auto set_item = [&]() {
       pos0 = seq - qlen + tile * TT;
@@ -266,49 +320,70 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                               bt_entry((kb + lane) * kKB / BS, p.a.ring_blocks))
                       : 0;
     };
-    bool more = r >= 0 && u_lo < u_hi;
+    bool more = u_lo < u_hi;
     int kb0 = 0, kb1 = 0, pages = 0;
     if (more) {
-      load_window(r);
-      set_request();
+      // placed by the host: the first copies wait only for their page ids
+      t0 = p.start[b].t0;
+      qlen = p.start[b].q_len;
+      seq = p.start[b].seq;
       set_item();
-      kb0 = kb_lo + (int)(u_lo - u0);
-      kb1 = kb_lo + (int)(min(u0 + nblk, u_hi) - u0);
+      kb0 = kb_lo + u_lo - u0;
+      kb1 = kb_lo + min(u0 + nblk, u_hi) - u0;
       pages = load_pages(r, kb0, min(32, kb1 - kb0));
     }
     while (more && ok) {
-      const int qs = k & 1;
-      if (k >= kMaxQueue &&
-          !mbar_wait_warp_or_abort(&sm.pempty[qs], (uint32_t)((k >> 1) - 1) & 1, &sm.abort_flag)) {
+      const int qs = k % kQueue;
+      if (k >= kQueue &&
+          !mbar_wait_warp_or_abort(&sm.pempty[qs], (uint32_t)(k / kQueue - 1) & 1, &sm.abort_flag)) {
         ok = false;
         break;
       }
       if (lane == 0) {
         Q8Piece& d = sm.piece[qs];
+        d.r = r;
         d.t0 = t0 + tile * TT;
         d.ntok = ntok;
         d.n = kb1 - kb0;
         d.kb0 = kb0;
         d.pos0 = pos0;
         d.slot = 2 * b + (k > 0 ? 1 : 0);  // pieces between the two are direct
-        d.direct = owner_of(u0, U, C) == owner_of(u0 + nblk - 1, U, C);
+        d.direct = u0 >= u_lo && u0 + nblk <= u_hi;
+        d.last = kb1 == kb_lo + nblk;
         mbar_arrive(&sm.pfull[qs]);
       }
       __syncwarp();
       ++k;
+      {
+        // the piece's query rows and new rows on their way into L1: under a full stream a load
+        // takes over a microsecond, which the consumers would wait for at every piece
+        const int elt = F32 ? 4 : 2, t = t0 + tile * TT;
+        const uint8_t* q = static_cast<const uint8_t*>(p.a.q);
+        const int row = p.a.num_q_heads * D * elt, part = (HB << p.lg_group) * D * elt;
+        for (int i = lane * 128; i < ntok * part; i += 32 * 128)
+          prefetch_l1(q + (long long)(t + i / part) * row + hg * part + i % part);
+        if (p.k_new != nullptr && kb1 == kb_lo + nblk) {
+          const long long at = ((long long)t * Hkv + hg * HB) * D * elt;
+          for (int i = lane * 128; i < HB * D * elt; i += 32 * 128) {
+            prefetch_l1(static_cast<const uint8_t*>(p.k_new) + at + i);
+            prefetch_l1(static_cast<const uint8_t*>(p.v_new) + at + i);
+          }
+          if (lane == 0) prefetch_l1(p.slot_mapping + t);
+          if (lane == 1) prefetch_l1(p.a.block_table + (long long)r * p.a.bt_stride + pos0 / BS);
+        }
+      }
       // the item after this one, looked up once this piece's first copy is out
       bool looked = false;
       int nr = r, n_kb0 = 0, n_kb1 = 0;
       const int cur_r = r, first = kb0, last = kb1;
-      const long long u_end = u0 + nblk;
+      const int u_end = u0 + nblk;
       for (int kb_base = first; kb_base < last && ok; kb_base += 32) {
         const int n = min(32, last - kb_base);
         const int cur = pages;
         for (int j = 0; j < n; ++j) {
           const int pg = __shfl_sync(0xffffffffu, cur, j);
-          const int s = i % p.stages;
-          if (i >= p.stages && !mbar_wait_warp_or_abort(&sm.empty[s], (uint32_t)((i / p.stages) - 1) & 1,
-                                                        &sm.abort_flag)) {
+          if (round > 0 && !mbar_wait_warp_or_abort(&sm.empty[s], (uint32_t)(round - 1) & 1,
+                                                    &sm.abort_flag)) {
             ok = false;
             break;
           }
@@ -334,6 +409,10 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
           }
           __syncwarp();
           ++i;
+          if (++s == p.stages) {
+            s = 0;
+            ++round;
+          }
           if (j == 0) {
             if (kb_base + 32 < last) {
               pages = load_pages(cur_r, kb_base + 32, min(32, last - kb_base - 32));
@@ -358,7 +437,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 u0 = u_end;
                 set_item();
                 n_kb0 = kb_lo;
-                n_kb1 = kb_lo + (int)(min(u0 + nblk, u_hi) - u0);
+                n_kb1 = kb_lo + min(u0 + nblk, u_hi) - u0;
                 pages = load_pages(r, n_kb0, min(32, n_kb1 - n_kb0));
               }
             }
@@ -369,9 +448,9 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       kb1 = n_kb1;
     }
     if (ok) {
-      const int qs = k & 1;
-      if (k >= kMaxQueue &&
-          !mbar_wait_warp_or_abort(&sm.pempty[qs], (uint32_t)((k >> 1) - 1) & 1, &sm.abort_flag))
+      const int qs = k % kQueue;
+      if (k >= kQueue &&
+          !mbar_wait_warp_or_abort(&sm.pempty[qs], (uint32_t)(k / kQueue - 1) & 1, &sm.abort_flag))
         ok = false;
       if (ok && lane == 0) {
         sm.piece[qs].t0 = -1;
@@ -399,35 +478,79 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       const int Hq = p.a.num_q_heads;
       const uint32_t stage0 = smem_u32(stages);
       const uint32_t scale0 = smem_u32(scales) + head;
-      // rows of this lane's keys and chunks within a staged block
-      const int key_a = key_of_row<D>(gid), key_b = key_of_row<D>(gid + 8);
-      uint32_t k_off[2], v_off[4];
-      if constexpr (D == 128) {
-        k_off[0] = row_chunk<D>(hl * kKB + key_a, 2 * tq);  // the other chunk: address ^ 16
-        k_off[1] = row_chunk<D>(hl * kKB + key_b, 2 * tq);
-      } else {
-        k_off[0] = row_chunk<D>(hl * kKB + key_a, tq);
-        k_off[1] = row_chunk<D>(hl * kKB + key_b, tq);
-      }
-      int v_key[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v_key[j] = key_of_row<D>(2 * tq + (j & 1) + (j >> 1) * 8);
-        v_off[j] = box_bytes + (D == 128 ? row_chunk<D>(hl * kKB + v_key[j], gid)
-                                         : row_chunk<D>(hl * kKB + v_key[j], gid >> 1) + (gid & 1) * 8);
-      }
-      int i0 = 0;          // block index of the piece's first block
-      int xphase = 0;      // exchange rounds so far
+      // This lane's pieces of a staged block. K: chunks of keys key_a and key_a + 8. V: keys
+      // key_of_row(2 tq) at v_off, the next row of the fragment 128 bytes on with bit 4 of the
+      // swizzled chunk turned, and the same two 8 keys further.
+      const int key_a = key_of_row<D>(gid);
+      const uint32_t k_off = D == 128 ? row_chunk<D>(hl * kKB + key_a, 2 * tq)
+                                      : row_chunk<D>(hl * kKB + key_a, tq);
+      const uint32_t v_off =
+          box_bytes + (D == 128 ? row_chunk<D>(hl * kKB + key_of_row<D>(2 * tq), gid)
+                                : row_chunk<D>(hl * kKB + key_of_row<D>(2 * tq), gid >> 1) + (gid & 1) * 8);
+      int i0 = 0;                // block index of the piece's first block
+      int s = kw, round = 0;     // stage and round of this warp's next block (kw, kw + KW, ...)
       for (int k = 0;; ++k) {
-        const int qs = k & 1;
-        if (!mbar_wait_warp_or_abort(&sm.pfull[qs], (uint32_t)(k >> 1) & 1, &sm.abort_flag)) {
+        if (!mbar_wait_warp_or_abort(&sm.pfull[k % kQueue], (uint32_t)(k / kQueue) & 1, &sm.abort_flag)) {
           give_up();
           return;
         }
-        const Q8Piece d = sm.piece[qs];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.pempty[qs]);
+        // The piece stays in its queue slot until this warp is done with it: its fields are read
+        // from shared memory where they are used, not held in registers across the key loop.
+        const volatile Q8Piece& d = sm.piece[k % kQueue];
         if (d.t0 < 0) break;
+        auto release_piece = [&]() {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.pempty[k % kQueue]);
+        };
+
+        // ---- the request's new row of this head, quantised by the warp that will read its block:
+        // lane l has values 4 l .. 4 l + 3 of K and of V (D 64: lanes 0 - 15 those of K, lanes
+        // 16 - 31 those of V)
+        const bool own_new = p.k_new != nullptr && d.last && (i0 + d.n - 1) % KW == kw;
+        if (own_new) {
+          const int t0 = d.t0, pos = d.pos0, BS = p.a.block_size;
+          long long slot = __ldg(p.slot_mapping + t0);
+          const int page = __ldg(p.a.block_table + (long long)d.r * p.a.bt_stride + pos / BS);
+          const long long at = ((long long)t0 * Hkv + head) * D + lane * 4 % D;
+          const int w = lane % (D / 4);
+          float x[4];
+          load4<F32>(D == 128 || lane < 16 ? p.k_new : p.v_new, at, x);
+          uint32_t a = magnitude4(x);
+          Q8NewRow& f = sm.fresh[warp];
+          if constexpr (D == 128) {
+            float y[4];
+            load4<F32>(p.v_new, at, y);
+            uint32_t c = magnitude4(y);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) {
+              a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
+              c = max(c, __shfl_xor_sync(0xffffffffu, c, off));
+            }
+            const int kc = e8m0_of_magnitude(a), vc = e8m0_of_magnitude(c);
+            f.k[w] = quantise4(x, e8m0_inverse(kc));
+            f.v[w] = quantise4(y, e8m0_inverse(vc));
+            if (lane == 0) {
+              f.k_code = kc;
+              f.v_code = vc;
+            }
+          } else {
+#pragma unroll
+            for (int off = 8; off > 0; off >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, off));
+            const int code = e8m0_of_magnitude(a);
+            (lane < 16 ? f.k : f.v)[w] = quantise4(x, e8m0_inverse(code));
+            if (lane == 0) f.k_code = code;
+            if (lane == 16) f.v_code = code;
+          }
+          if (slot >= (long long)p.a.num_blocks * BS) {
+            if (lane == 0) record_error(p.a.error_word, CB_DEVERR_SLOT);
+            slot = -1;
+          }
+          if (lane == 0) {
+            f.row = slot < 0 ? -1 : slot * Hkv + head;
+            f.staged = slot == (long long)page * BS + pos % BS;
+          }
+          __syncwarp();
+        }
 
         // ---- q: column 8 nb + gid, d = D/4 tq .. + D/4 - 1, as fp16 fragments
         uint32_t qf[NB][kKS][2 * kSplit];
@@ -439,34 +562,24 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
           const bool live = tok < d.ntok;
           const long long at =
               ((long long)(d.t0 + tok) * Hq + head * G + (col & (G - 1))) * D + tq * (D / 4);
-          float x[D / 4];
-          if constexpr (F32) {
-            const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.a.q) + at);
+          constexpr int kRaw = F32 ? D / 4 : D / 8;  // words: fp32 values, or bf16 pairs
+          uint32_t raw[kRaw];
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.a.q) + at * (F32 ? 4 : 2));
 #pragma unroll
-            for (int e = 0; e < D / 16; ++e) {
-              const float4 v = live ? __ldg(src + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-              x[4 * e] = v.x;
-              x[4 * e + 1] = v.y;
-              x[4 * e + 2] = v.z;
-              x[4 * e + 3] = v.w;
-            }
-          } else {
-            const uint4* src =
-                reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) + at);
-#pragma unroll
-            for (int e = 0; e < D / 32; ++e) {
-              const uint4 v = live ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                x[8 * e + 2 * c] = __uint_as_float(w[c] << 16);
-                x[8 * e + 2 * c + 1] = __uint_as_float(w[c] & 0xffff0000u);
-              }
-            }
+          for (int e = 0; e < kRaw / 4; ++e) {
+            const uint4 v = live ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
+            raw[4 * e] = v.x;
+            raw[4 * e + 1] = v.y;
+            raw[4 * e + 2] = v.z;
+            raw[4 * e + 3] = v.w;
           }
+          auto value = [&](int e) -> float {  // of d = D/4 tq + e
+            if constexpr (F32) return __uint_as_float(raw[e]);
+            return __uint_as_float(e & 1 ? raw[e / 2] & 0xffff0000u : raw[e / 2] << 16);
+          };
           uint32_t top = 0u;
 #pragma unroll
-          for (int e = 0; e < D / 4; ++e) top = max(top, finite_magnitude(x[e]));
+          for (int e = 0; e < D / 4; ++e) top = max(top, finite_magnitude(value(e)));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
           const int ex = top == 0u ? 13 : max((int)(top >> 23) - 127, -100);
@@ -478,7 +591,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
           for (int ks = 0; ks < kKS; ++ks) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float lo = x[4 * ks + 2 * e] * up, hi = x[4 * ks + 2 * e + 1] * up;
+              const float lo = value(4 * ks + 2 * e) * up, hi = value(4 * ks + 2 * e + 1) * up;
               qf[nb][ks][e] = pack_f16x2(lo, hi);
               if constexpr (F32) qf[nb][ks][2 + e] = pack_f16x2_rest(qf[nb][ks][e], lo, hi);
             }
@@ -494,31 +607,63 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
           m[nb][0] = m[nb][1] = mw[nb][0] = mw[nb][1] = kNoMax;
           l[nb][0] = l[nb][1] = 0.f;
         }
-        // keys every column attends: [all_lo, all_hi]; keys any column attends: [any_lo, any_hi]
-        const int any_lo = first_key(d.pos0, W), any_hi = d.pos0 + d.ntok - 1;
-        const int all_lo = first_key(any_hi, W), all_hi = d.pos0;
-
+        // blocks inside this range lie inside every column's: no masks
+        const int inner_lo = first_key(d.pos0 + d.ntok - 1, W), inner_hi = d.pos0;
         // this warp's blocks: global block indices congruent to kw modulo KW
-        for (int j = (kw - i0 % KW + KW) % KW; j < d.n; j += KW) {
-          const int i = i0 + j;
-          const int s = i % p.stages;
-          if (!mbar_wait_warp_or_abort(&sm.full[s], (uint32_t)(i / p.stages) & 1, &sm.abort_flag)) {
+        const int n = d.n, base = d.kb0 * kKB;
+        for (int j = (kw - i0 % KW + KW) % KW; j < n; j += KW) {
+          if (!mbar_wait_warp_or_abort(&sm.full[s], (uint32_t)round & 1, &sm.abort_flag)) {
             give_up();
             return;
           }
           const uint32_t st = stage0 + s * stage_bytes;
           const uint32_t sc = scale0 + s * 2 * scale_bytes;
-          const int key_base = (d.kb0 + j) * kKB;
-          const int ka = key_base + key_a, kb = key_base + key_b;
-
+          uint64_t* const done = &sm.empty[s];
+          s += KW;
+          if (s >= p.stages) {
+            s -= p.stages;
+            ++round;
+          }
+          const int key_base = base + j * kKB;
+          const int ka = key_base + key_a, kb = ka + 8;
+          if (own_new && j == n - 1) {
+            const Q8NewRow& f = sm.fresh[warp];
+            const int w = lane % (D / 4);
+            if (f.row >= 0) {
+              if (f.staged) {  // over the stale row in the staged block
+                const int key = d.pos0 - key_base;
+                const uint32_t at = row_chunk<D>(hl * kKB + key, w / 4) + (w & 3) * 4;
+                sts32(st + at, f.k[w]);
+                sts32(st + box_bytes + at, f.v[w]);
+                if (lane == 0) {
+                  sts8(sc + key * Hkv, f.k_code);
+                  sts8(sc + scale_bytes + key * Hkv, f.v_code);
+                }
+                // the producer's next copies into this stage come after these stores
+                fence_proxy_async_smem();
+              }
+              *reinterpret_cast<uint32_t*>(p.c.k + f.row * D + w * 4) = f.k[w];
+              *reinterpret_cast<uint32_t*>(p.c.v + f.row * D + w * 4) = f.v[w];
+              if (lane == 0) {
+                p.c.k_scale[f.row] = (uint8_t)f.k_code;
+                p.c.v_scale[f.row] = (uint8_t)f.v_code;
+              }
+            }
+            __syncwarp();
+          }
           // ---- S^T = K Q^T
-          float sa[NB][4];
+          // (in two chains, even and odd steps: half the dependent latency; fp32 queries keep
+          // their low parts in a third, where the truncation of the large sums does not reach them)
+          constexpr int kChains = F32 ? 3 : 2;
+          float sc_[kChains][NB][4];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) sa[nb][0] = sa[nb][1] = sa[nb][2] = sa[nb][3] = 0.f;
+          for (int c = 0; c < kChains; ++c)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) sc_[c][nb][0] = sc_[c][nb][1] = sc_[c][nb][2] = sc_[c][nb][3] = 0.f;
 #pragma unroll
           for (int half = 0; half < D / 64; ++half) {
-            const uint4 va = lds128(st + (k_off[0] ^ (half << 4)));
-            const uint4 vb = lds128(st + (k_off[1] ^ (half << 4)));
+            const uint4 va = lds128(st + (k_off ^ (half << 4)));
+            const uint4 vb = lds128(st + (k_off ^ (half << 4)) + 8 * D);
             const uint32_t wa[4] = {va.x, va.y, va.z, va.w};
             const uint32_t wb[4] = {vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
@@ -527,19 +672,27 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
                 const uint32_t(&q)[2 * kSplit] = qf[nb][4 * half + e];
-                mma_f16_16816(sa[nb], a, q[0], q[1]);
-                if constexpr (F32) mma_f16_16816(sa[nb], a, q[2], q[3]);
+                mma_f16_16816(sc_[e & 1][nb], a, q[0], q[1]);
+                if constexpr (F32) mma_f16_16816(sc_[2][nb], a, q[2], q[3]);
               }
             }
           }
+          float sa[NB][4];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              sa[nb][e] = sc_[0][nb][e] + sc_[1][nb][e];
+              if constexpr (F32) sa[nb][e] += sc_[2][nb][e];
+            }
           // ---- scales: 2^ek on the score, ev in the weight's exponent
           const float fa = e8m0_value(lds_u8(sc + key_a * Hkv));
-          const float fb = e8m0_value(lds_u8(sc + key_b * Hkv));
+          const float fb = e8m0_value(lds_u8(sc + (key_a + 8) * Hkv));
           const int ca = lds_u8(sc + scale_bytes + key_a * Hkv);
-          const int cb_ = lds_u8(sc + scale_bytes + key_b * Hkv);
+          const int cb_ = lds_u8(sc + scale_bytes + (key_a + 8) * Hkv);
           const float ea = ca == 255 ? __uint_as_float(0x7fc00000u) : (float)(ca - kE8m0Bias);
           const float eb = cb_ == 255 ? __uint_as_float(0x7fc00000u) : (float)(cb_ - kE8m0Bias);
-          const bool edge = key_base < all_lo || key_base + kKB - 1 > all_hi;  // warp-uniform
+          const bool edge = key_base < inner_lo || key_base + kKB - 1 > inner_hi;  // warp-uniform
           uint32_t pw[NB][2 * kSplit];
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
@@ -604,46 +757,99 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             if constexpr (D == 128) {
-              const uint4 x = lds128(st + v_off[r]);
+              const uint4 x = lds128(st + (v_off ^ ((r & 1) << 4)) + (r & 1) * 128 + (r >> 1) * 8 * D);
               v[r][0] = x.x;
               v[r][1] = x.y;
               v[r][2] = x.z;
               v[r][3] = x.w;
             } else {
-              const uint2 x = lds64(st + v_off[r]);
+              const uint2 x = lds64(st + (v_off ^ ((r & 1) << 4)) + (r & 1) * 128 + (r >> 1) * 8 * D);
               v[r][0] = x.x;
               v[r][1] = x.y;
             }
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm.empty[s]);
-          if (key_base < any_lo || key_base + kKB - 1 > any_hi) {
+          if (lane == 0) mbar_arrive(done);
+          if (edge) {
             // slots no row of the item attends hold anything, NaN codes too: weight 0 x value 0
+            const int lo = first_key(d.pos0, W), hi = d.pos0 + d.ntok - 1;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const int key = key_base + v_key[r];
-              if (key < any_lo || key > any_hi)
+              const int key = key_base + key_of_row<D>(2 * tq + (r & 1)) + (r >> 1) * 8;
+              if (key < lo || key > hi)
 #pragma unroll
                 for (int e = 0; e < D / 32; ++e) v[r][e] = 0u;
+            }
+          }
+          if (edge && d.ntok > 1) {
+            // A NaN value reaches only the rows that attend its key: it is taken out of the product
+            // (weight 0 x NaN), and the outputs of the rows that do attend it are set by a product
+            // of indicators.
+            uint32_t any = 0u;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int e = 0; e < D / 32; ++e) any |= nan_bytes(v[r][e]);
+            if (__any_sync(0xffffffffu, any != 0u)) {
+              uint32_t at[NB][2];
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) {
+                const int h0 = d.pos0 + ((8 * nb + 2 * tq) >> p.lg_group);
+                const int h1 = d.pos0 + ((8 * nb + 2 * tq + 1) >> p.lg_group);
+                const int l0 = first_key(h0, W), l1 = first_key(h1, W);
+                const float a0 = ka >= l0 && ka <= h0 ? 1.f : 0.f, a1 = ka >= l1 && ka <= h1 ? 1.f : 0.f;
+                const float b0 = kb >= l0 && kb <= h0 ? 1.f : 0.f, b1 = kb >= l1 && kb <= h1 ? 1.f : 0.f;
+                at[nb][0] = movmatrix_trans(pack_f16x2(a0, a1));
+                at[nb][1] = movmatrix_trans(pack_f16x2(b0, b1));
+              }
+#pragma unroll
+              for (int e = 0; e < D / 32; ++e)
+#pragma unroll
+                for (int hi = 0; hi < 2; ++hi) {
+                  constexpr uint32_t kOne = 0x38383838u;  // 1.0 in e4m3
+                  uint32_t a[4];
+                  v_fragment(a, nan_bytes(v[0][e]) & kOne, nan_bytes(v[1][e]) & kOne,
+                             nan_bytes(v[2][e]) & kOne, nan_bytes(v[3][e]) & kOne, hi);
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb) {
+                    float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_f16_16816(hit, a, at[nb][0], at[nb][1]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                      if (hit[c] > 0.f) o[nb][2 * e + hi][c] = __uint_as_float(0x7fc00000u);
+                  }
+                }
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int e = 0; e < D / 32; ++e) v[r][e] &= ~nan_bytes(v[r][e]);
             }
           }
 #pragma unroll
           for (int e = 0; e < D / 32; ++e) {
 #pragma unroll
             for (int hi = 0; hi < 2; ++hi) {
-              const uint32_t sel = hi ? 0x7362u : 0x5140u;  // bytes of two keys side by side
-              const uint32_t x = __byte_perm(v[0][e], v[1][e], sel);
-              const uint32_t y = __byte_perm(v[2][e], v[3][e], sel);
-              const uint32_t a[4] = {f16x2_lo(x), f16x2_hi(x), f16x2_lo(y), f16x2_hi(y)};
+              uint32_t a[4];
+              v_fragment(a, v[0][e], v[1][e], v[2][e], v[3][e], hi);
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
-                mma_f16_16816(o[nb][2 * e + hi], a, pw[nb][0], pw[nb][1]);
-                if constexpr (F32) mma_f16_16816(o[nb][2 * e + hi], a, pw[nb][2], pw[nb][3]);
+                float(&acc)[4] = o[nb][2 * e + hi];
+                if constexpr (F32) {
+                  // the block's sum by itself, then added rounded to nearest: the tensor cores
+                  // truncate, which over a long context would add up to a bias
+                  float t[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma_f16_16816(t, a, pw[nb][2], pw[nb][3]);
+                  mma_f16_16816(t, a, pw[nb][0], pw[nb][1]);
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) acc[c] += t[c];
+                } else {
+                  mma_f16_16816(acc, a, pw[nb][0], pw[nb][1]);
+                }
               }
             }
           }
         }
-        i0 += d.n;
+        i0 += n;
 
         // ---- the end of the piece: sums over the key rows of the columns
 #pragma unroll
@@ -655,72 +861,59 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
               l[nb][c] += __shfl_xor_sync(0xffffffffu, l[nb][c], off);
         // ---- join the KW warps of the head: warp 0 takes the others' states in rounds
         if (KW > 1) {
-          constexpr int kRounds = NB * kKS * 4 / kXRegs;
           float* of = &o[0][0][0];
           if (kw > 0) {
             const int xs = (kw - 1) * HB + hl;
             float* x = xchg + xs * kXFloats + lane;
-#pragma unroll
-            for (int rd = 0; rd < kRounds; ++rd) {
-              const int ph = xphase + rd;
-              if (ph > 0 && !mbar_wait_warp_or_abort(&sm.xempty[xs], (uint32_t)(ph - 1) & 1, &sm.abort_flag)) {
-                give_up();
-                return;
-              }
-              if (rd == 0) {
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                  for (int c = 0; c < 2; ++c) {
-                    x[(6 * nb + 3 * c) * 32] = m[nb][c];
-                    x[(6 * nb + 3 * c + 1) * 32] = mw[nb][c];
-                    x[(6 * nb + 3 * c + 2) * 32] = l[nb][c];
-                  }
-              }
-#pragma unroll
-              for (int e = 0; e < kXRegs; ++e) x[(6 * NB + e) * 32] = of[rd * kXRegs + e];
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sm.xfull[xs]);
+            if (k > 0 && !mbar_wait_warp_or_abort(&sm.xempty[xs], (uint32_t)(k - 1) & 1, &sm.abort_flag)) {
+              give_up();
+              return;
             }
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                x[(6 * nb + 3 * c) * 32] = m[nb][c];
+                x[(6 * nb + 3 * c + 1) * 32] = mw[nb][c];
+                x[(6 * nb + 3 * c + 2) * 32] = l[nb][c];
+              }
+#pragma unroll
+            for (int e = 0; e < kORegs; ++e) x[(6 * NB + e) * 32] = of[e];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.xfull[xs]);
           } else {
             for (int w = 1; w < KW; ++w) {
               const int xs = (w - 1) * HB + hl;
               const float* x = xchg + xs * kXFloats + lane;
-              float own[NB][2], other[NB][2];
-#pragma unroll
-              for (int rd = 0; rd < kRounds; ++rd) {
-                const int ph = xphase + rd;
-                if (!mbar_wait_warp_or_abort(&sm.xfull[xs], (uint32_t)ph & 1, &sm.abort_flag)) {
-                  give_up();
-                  return;
-                }
-                if (rd == 0) {
-#pragma unroll
-                  for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                      const float mo = x[(6 * nb + 3 * c) * 32], wo = x[(6 * nb + 3 * c + 1) * 32];
-                      const float mn = fmaxf(m[nb][c], mo), wn = fmaxf(mw[nb][c], wo);
-                      l[nb][c] = l[nb][c] * ex2_approx(m[nb][c] - mn) +
-                                 x[(6 * nb + 3 * c + 2) * 32] * ex2_approx(mo - mn);
-                      own[nb][c] = ex2_approx(mw[nb][c] - wn);
-                      other[nb][c] = ex2_approx(wo - wn);
-                      m[nb][c] = mn;
-                      mw[nb][c] = wn;
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < kXRegs; ++e) {
-                  const int at = rd * kXRegs + e, nb = at / (kKS * 4), c = at & 1;
-                  of[at] = of[at] * own[nb][c] + x[(6 * NB + e) * 32] * other[nb][c];
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.xempty[xs]);
+              if (!mbar_wait_warp_or_abort(&sm.xfull[xs], (uint32_t)k & 1, &sm.abort_flag)) {
+                give_up();
+                return;
               }
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  const float mo = x[(6 * nb + 3 * c) * 32], wo = x[(6 * nb + 3 * c + 1) * 32];
+                  const float mn = fmaxf(m[nb][c], mo), wn = fmaxf(mw[nb][c], wo);
+                  l[nb][c] = l[nb][c] * ex2_approx(m[nb][c] - mn) +
+                             x[(6 * nb + 3 * c + 2) * 32] * ex2_approx(mo - mn);
+                  const float own = ex2_approx(mw[nb][c] - wn), other = ex2_approx(wo - wn);
+                  m[nb][c] = mn;
+                  mw[nb][c] = wn;
+#pragma unroll
+                  for (int e = 0; e < kKS; ++e)
+#pragma unroll
+                    for (int h = c; h < 4; h += 2)
+                      o[nb][e][h] = o[nb][e][h] * own + x[(6 * NB + (nb * kKS + e) * 4 + h) * 32] * other;
+                }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sm.xempty[xs]);
             }
           }
-          xphase += kRounds;
-          if (kw > 0) continue;
+          if (kw > 0) {
+            release_piece();
+            continue;
+          }
         }
         // ---- write: column 8 nb + 2 tq + c, outputs d = D/8 gid .. + D/8 - 1 of this lane
 #pragma unroll
@@ -764,6 +957,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
           }
         }
+        release_piece();
       }
     };
     consume();
@@ -942,7 +1136,7 @@ cudaError_t launch_portable_t(const StepArgs& a, const Q8Cache& c, cudaStream_t 
 
 size_t q8_smem_bytes(int D, int HB, int KW, int NB, int stages, int Hkv) {
   return 1024 /* alignment slack */ + (size_t)stages * (2 * HB * kKB * D + 2 * kKB * Hkv) +
-         (size_t)(KW - 1) * HB * (6 * NB + 16) * 128 /* exchange slots */ + sizeof(Q8Smem);
+         (size_t)(KW - 1) * HB * (6 + D / 4) * NB * 128 /* exchange slots */ + sizeof(Q8Smem);
 }
 
 cudaError_t launch_q8_split(const Q8Args& p, int column_blocks, cudaStream_t stream) {

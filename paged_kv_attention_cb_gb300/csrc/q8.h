@@ -35,30 +35,41 @@ constexpr int kQ8MaxStages = 32;
 constexpr int kQ8MaxHeads = 8;       // KV heads per CTA
 constexpr int kQ8TableCtas = 192;    // CTAs per group of heads (their starts are arguments)
 constexpr int kQ8SmemLimit = 232448; // 227 KiB dynamic shared memory per CTA
+// Bytes of the ring: a little over the latency times the rate of one SM's share of HBM. More
+// only takes L1 away from the query rows and the few spilled registers (16 requests x 32768: 168
+// us with 132 KB of stages, 177 with 198 KB, 211 with 66 KB).
+constexpr int kQ8RingBytes = 136 * 1024;
 constexpr int kQ8MinBlocksPerCta = 4;
 
-// Where a CTA's range of key blocks starts.
+// Where a CTA's range of key blocks starts (the entry behind the last CTA: the end of all).
 struct Q8CtaStart {
-  int r;     // request (-1: none)
-  int tile;  // token tile within the request
+  int u;     // global index of the CTA's first key block
+  int r;     // its request
+  int tile;  // its token tile within the request
   int u0;    // global index of that item's first key block
+  int t0, q_len, seq;  // the request's first query row, query tokens and KV length
 };
 
 struct Q8Args {
   StepArgs a;  // k_cache / v_cache unused
   Q8Cache c;
-  int total_units;    // U: key blocks of all items
-  int num_ctas;       // C: CTA b takes blocks [b U / C, (b + 1) U / C)
+  int num_ctas;       // CTA b takes the key blocks from start[b].u to start[b + 1].u
   int heads_per_cta;  // HB
   int key_warps;      // KW: warps per KV head; block i goes to warp i % KW
   int stages;         // multiple of KW
   int tile_tokens;    // TT: query tokens per item (TT * G columns, at most 8 NB)
   int lg_group;       // log2 of query heads per KV head
   int max_q;
+  // Steps of decode rows only: the warp that reads a request's last key block quantises the
+  // request's new row of its head into the cache and into its staged copy of the block, so the
+  // step needs no launch of its own for the write. nullptr: the rows are in the cache already.
+  const void* k_new;  // [T, Hkv, D]
+  const void* v_new;
+  const int64_t* slot_mapping;
   float* part_o;      // [slot * TT + token][Hq][D]: CTA b's first piece has slot 2 b, its last
                       // 2 b + 1 (an item between them lies in the CTA and is written directly)
   float2* part_ml;    // [slot * TT + token][Hq]
-  Q8CtaStart start[kQ8TableCtas];
+  Q8CtaStart start[kQ8TableCtas + 1];
 };
 
 // Column blocks (of 8 columns) a CTA's items have: 1, 2 or 4; fp32 queries at most 2.

@@ -56,6 +56,7 @@ size_t scratch_bytes(int64_t table_pages, int64_t pages, int block_size, int Hkv
 
 struct Q8Plan {
   bool split = false;
+  bool decode_only = false;  // every request has at most one query row
   int column_blocks = 1;
   cb::Q8Args args;
   std::vector<cb::MergeRow> merge;
@@ -76,6 +77,7 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
   }
   if (longest == 0) return;
   plan.split = true;
+  plan.decode_only = longest == 1 && plan.chunks.empty();
   const int top = a.dtype == CB_F32 ? 2 : 4;  // column blocks (fp32 queries: twice the operands)
   int nb = 1;
   while (nb < top && 8 * nb < std::min<int64_t>((int64_t)longest * G, kMaxColumns)) nb *= 2;
@@ -95,7 +97,7 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
   while (p.key_warps < 8 && 2 * p.key_warps * HB <= (nb == 1 ? 16 : 8)) p.key_warps *= 2;
   const size_t fixed = cb::q8_smem_bytes(a.head_dim, HB, p.key_warps, nb, 0, a.num_kv_heads);
   const size_t per = cb::q8_smem_bytes(a.head_dim, HB, p.key_warps, nb, 1, a.num_kv_heads) - fixed;
-  p.stages = (int)std::min<size_t>(cb::kQ8MaxStages, (cb::kQ8SmemLimit - fixed) / per);
+  p.stages = (int)std::min({(size_t)cb::kQ8MaxStages, (cb::kQ8SmemLimit - fixed) / per, cb::kQ8RingBytes / per});
   p.stages -= p.stages % p.key_warps;
 
   const int TT = p.tile_tokens, W = a.sliding_window;
@@ -114,7 +116,6 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
   const int groups = a.num_kv_heads / HB;
   long long C = std::max(1, std::min(cb::sm_count(), cb::kQ8TableCtas) / groups);
   C = std::min(C, (U + cb::kQ8MinBlocksPerCta - 1) / cb::kQ8MinBlocksPerCta);
-  p.total_units = (int)U;
   p.num_ctas = (int)C;
 
   // where each CTA's range starts, and the items that several CTAs share
@@ -123,7 +124,7 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
   int b = 0;
   each_item([&](int r, int tile, int pos0, int ntok) {
     const int n = blocks(pos0, ntok);
-    for (; b < C && start_of(b) < u + n; ++b) p.start[b] = cb::Q8CtaStart{r, tile, (int)u};
+    for (; b < C && start_of(b) < u + n; ++b) p.start[b] = cb::Q8CtaStart{(int)start_of(b), r, tile, (int)u, qsl[r], qsl[r + 1] - qsl[r], seq_lens[r]};
     const int b0 = (int)(((u + 1) * C + U - 1) / U) - 1;
     const int b1 = (int)(((u + n) * C + U - 1) / U) - 1;
     if (b1 > b0) {
@@ -135,6 +136,9 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
     }
     u += n;
   });
+  p.start[C] = cb::Q8CtaStart{(int)U, -1, 0, 0, 0, 0, 0};
+  p.k_new = p.v_new = nullptr;
+  p.slot_mapping = nullptr;
   const Layout w = layout_of(a.num_kv_heads, a.head_dim);
   p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
@@ -333,10 +337,15 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
     plan_split(plan, a, c, max_q, h_query_start_loc, h_seq_lens, ws);
   }
   cudaError_t e = cudaSuccess;
-  if (k_new)
+  if (k_new && fast && plan.split && plan.decode_only) {
+    plan.args.k_new = k_new;
+    plan.args.v_new = v_new;
+    plan.args.slot_mapping = slot_mapping;
+  } else if (k_new) {
     e = cb::launch_write_kv_q8(k_new, v_new, c, slot_mapping, num_tokens,
                                (int64_t)num_blocks * block_size, num_kv_heads, head_dim, dtype,
                                a.error_word, s);
+  }
   if (e != cudaSuccess) return cb::report_cuda_error(e, "write_kv_q8 launch");
   if (!fast) {
     e = cb::launch_q8_portable(a, c, s);

@@ -427,3 +427,43 @@ def test_binding_refuses():
         cb.paged_attention_q8(out, st.dq, *st.d, *args, k_new=st.dk)
     with pytest.raises(cb.CbError):
         cb.write_kv_q8(st.dk, st.dv, *st.d, st.md["slot_mapping"].int())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_nan_reaches_only_the_rows_that_attend_it(D, dtype):
+    """A NaN in one token's V row: the earlier tokens of the same run stay finite, the ones that
+    attend it are NaN in that element and nowhere else."""
+    for n, W in ((2, 0), (5, 0), (5, 3), (13, 0)):
+        spec = spec_of([n, 1], [21, 60], num_q_heads=4, num_kv_heads=2, head_dim=D, dtype=dtype, sliding_window=W, seed=n)
+        st = Q8Step(spec, seed=n)
+        clean = st.run().clone()
+        st.v_new[n // 2, 1, 37] = float("nan")
+        st.upload()
+        got = st.run()
+        pos = np.arange(n)
+        hit = torch.from_numpy((pos >= n // 2) & ((W == 0) | (pos - n // 2 < W)))
+        want = torch.zeros(got.shape, dtype=torch.bool)
+        want[:n, 2:, 37] = hit[:, None]
+        assert torch.equal(torch.isnan(got).cpu(), want)
+        assert torch.equal(got[~want.cuda()], clean[~want.cuda()])
+
+
+def test_new_rows_go_where_their_slots_say():
+    """Decode rows with a slot of -1, one in a page of nobody and one past the pool: the cache and
+    the attended values are those of a write before the attention."""
+    spec = spec_of([1, 1, 1, 1], [40, 21, 100, 3], seed=3)
+    spec.slot_mapping[1] = -1
+    spare = sorted(set(range(2, spec.num_blocks)) - set(spec.block_table.reshape(-1).tolist()))
+    spec.slot_mapping[2] = spare[0] * 16 + 5
+    st = Q8Step(spec, seed=3)
+    st.check(st.run())
+    st.check_cache()
+    assert cb.read_error_word(st.ws) == 0
+    spec.slot_mapping[3] = spec.num_blocks * 16
+    st = Q8Step(spec, seed=3)
+    out = st.run()
+    assert cb.read_error_word(st.ws) == cb.CB_DEVERR_SLOT
+    spec.slot_mapping[3] = -1  # skipped: as if it had none
+    st.check(out)
+    st.check_cache()
