@@ -15,8 +15,8 @@
 //
 // * Partition. The (request, tile of query tokens) items' 16-key blocks are numbered in
 //   request order and CTA b of C takes blocks [b U / C, (b + 1) U / C): equal bytes per CTA.
-//   An item inside one CTA is written directly; a piece of a longer one becomes a partial row
-//   that the merge kernel joins (merge.h).
+//   Each warp's share of an item in a CTA (a piece) becomes a partial row that the merge kernel
+//   joins (merge.h); only an item that one warp per head has to itself is written directly.
 // * Staging. A producer warp brings each block (16 keys, up to 8 KV heads, K and V) with two
 //   swizzled tensor copies and its scales with two bulk copies into a ring of stages.
 // * Operands. e4m3 is exact in fp16, so the contractions are fp16 mma.sync with fp32
@@ -36,9 +36,10 @@
 //   scale on an unattended key would push the attended ones' weights under fp16's range. Both
 //   are raised only when exceeded by more than 2^8, which a warp vote finds without the
 //   cross-lane maximum. Statistics, sums and outputs are fp32.
-// * Warps. KW warps share a KV head and take the blocks in turn, each with its own state;
-//   they join through shared memory at the end of an item's piece. At 8 heads and two warps
-//   each, one warp has ~1400 cycles per 16-key block at the HBM rate.
+// * Warps. KW warps share a KV head and take the blocks in turn, each with its own state and its
+//   own partial rows: a join through shared memory at the end of each piece cost 1.5 us there,
+//   in which the stream stood still, and the merge kernel has to run anyway. At 8 heads and two
+//   warps each, one warp has ~1400 cycles per 16-key block at the HBM rate.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <float.h>
@@ -67,8 +68,8 @@ struct Q8Piece {
   int n;       // key blocks of this piece
   int kb0;     // first of them
   int pos0;    // position of the first token
-  int slot;    // partial slot: 2 b for CTA b's first piece, 2 b + 1 for its last
-  int direct;  // the whole item lies in this CTA
+  int slot;    // partial slot (item + CTA)
+  int direct;  // the whole item is one warp's per head
   int last;    // the piece ends with the item's last key block
 };
 
@@ -85,8 +86,6 @@ struct Q8Smem {
   uint64_t empty[kQ8MaxStages];
   uint64_t pfull[kQueue];
   uint64_t pempty[kQueue];
-  uint64_t xfull[16];   // exchange slot written by warp (key warp, head)
-  uint64_t xempty[16];  // and read
   Q8Piece piece[kQueue];
   Q8NewRow fresh[16];  // by consumer warp: the warps of a head may be pieces apart
   int abort_flag;
@@ -225,10 +224,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
   const int scale_bytes = kKB * Hkv;       // K (or V) scales of one block, every head
   uint8_t* stages = base;
   uint8_t* scales = stages + p.stages * stage_bytes;
-  float* xchg = reinterpret_cast<float*>(scales + p.stages * 2 * scale_bytes);
-  constexpr int kORegs = NB * kKS * 4;      // outputs of a lane
-  constexpr int kXFloats = (6 * NB + kORegs) * 32;
-  Q8Smem& sm = *reinterpret_cast<Q8Smem*>(xchg + (KW - 1) * HB * kXFloats);
+  Q8Smem& sm = *reinterpret_cast<Q8Smem*>(scales + p.stages * 2 * scale_bytes);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -246,10 +242,6 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
     for (int s = 0; s < kQueue; ++s) {
       mbar_init(&sm.pfull[s], 1);
       mbar_init(&sm.pempty[s], nwarps);
-    }
-    for (int s = 0; s < 16; ++s) {
-      mbar_init(&sm.xfull[s], 1);
-      mbar_init(&sm.xempty[s], 1);
     }
     sm.abort_flag = 0;
     fence_barrier_init();
@@ -299,7 +291,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       return -1;
     };
     // the current item: its request's fields, its first block and its block count
-    int r = p.start[b].r, tile = p.start[b].tile;
+    int r = p.start[b].r, tile = p.start[b].tile, item = p.start[b].item;
     int u0 = p.start[b].u0;
     int t0 = 0, qlen = 0, seq = 0, pos0 = 0, ntok = 0, nblk = 0, kb_lo = 0;
     auto set_item = [&]() {
@@ -347,8 +339,8 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
         d.n = kb1 - kb0;
         d.kb0 = kb0;
         d.pos0 = pos0;
-        d.slot = 2 * b + (k > 0 ? 1 : 0);  // pieces between the two are direct
-        d.direct = u0 >= u_lo && u0 + nblk <= u_hi;
+        d.slot = item + b;
+        d.direct = KW == 1 && u0 >= u_lo && u0 + nblk <= u_hi;
         d.last = kb1 == kb_lo + nblk;
         mbar_arrive(&sm.pfull[qs]);
       }
@@ -434,6 +426,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
               }
               if (more) {
+                ++item;
                 u0 = u_end;
                 set_item();
                 n_kb0 = kb_lo;
@@ -859,62 +852,6 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1)
               l[nb][c] += __shfl_xor_sync(0xffffffffu, l[nb][c], off);
-        // ---- join the KW warps of the head: warp 0 takes the others' states in rounds
-        if (KW > 1) {
-          float* of = &o[0][0][0];
-          if (kw > 0) {
-            const int xs = (kw - 1) * HB + hl;
-            float* x = xchg + xs * kXFloats + lane;
-            if (k > 0 && !mbar_wait_warp_or_abort(&sm.xempty[xs], (uint32_t)(k - 1) & 1, &sm.abort_flag)) {
-              give_up();
-              return;
-            }
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                x[(6 * nb + 3 * c) * 32] = m[nb][c];
-                x[(6 * nb + 3 * c + 1) * 32] = mw[nb][c];
-                x[(6 * nb + 3 * c + 2) * 32] = l[nb][c];
-              }
-#pragma unroll
-            for (int e = 0; e < kORegs; ++e) x[(6 * NB + e) * 32] = of[e];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sm.xfull[xs]);
-          } else {
-            for (int w = 1; w < KW; ++w) {
-              const int xs = (w - 1) * HB + hl;
-              const float* x = xchg + xs * kXFloats + lane;
-              if (!mbar_wait_warp_or_abort(&sm.xfull[xs], (uint32_t)k & 1, &sm.abort_flag)) {
-                give_up();
-                return;
-              }
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  const float mo = x[(6 * nb + 3 * c) * 32], wo = x[(6 * nb + 3 * c + 1) * 32];
-                  const float mn = fmaxf(m[nb][c], mo), wn = fmaxf(mw[nb][c], wo);
-                  l[nb][c] = l[nb][c] * ex2_approx(m[nb][c] - mn) +
-                             x[(6 * nb + 3 * c + 2) * 32] * ex2_approx(mo - mn);
-                  const float own = ex2_approx(mw[nb][c] - wn), other = ex2_approx(wo - wn);
-                  m[nb][c] = mn;
-                  mw[nb][c] = wn;
-#pragma unroll
-                  for (int e = 0; e < kKS; ++e)
-#pragma unroll
-                    for (int h = c; h < 4; h += 2)
-                      o[nb][e][h] = o[nb][e][h] * own + x[(6 * NB + (nb * kKS + e) * 4 + h) * 32] * other;
-                }
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sm.xempty[xs]);
-            }
-          }
-          if (kw > 0) {
-            release_piece();
-            continue;
-          }
-        }
         // ---- write: column 8 nb + 2 tq + c, outputs d = D/8 gid .. + D/8 - 1 of this lane
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -947,7 +884,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 }
               }
             } else {
-              const long long row = ((long long)d.slot * TT + tok) * Hq + h;
+              const long long row = (((long long)d.slot * KW + kw) * TT + tok) * Hq + h;
               float4* out = reinterpret_cast<float4*>(p.part_o + row * D + gid * (D / 8));
 #pragma unroll
               for (int e = 0; e < kKS; e += 2)
@@ -1093,7 +1030,7 @@ cudaError_t cache_map(CUtensorMap* map, void* cache, const StepArgs& a, int hb) 
 template <int D, int NB, bool F32>
 cudaError_t launch_split_t(const Q8Args& p, cudaStream_t s) {
   auto kern = q8_split_kernel<D, NB, F32>;
-  const size_t smem = q8_smem_bytes(D, p.heads_per_cta, p.key_warps, NB, p.stages, p.a.num_kv_heads);
+  const size_t smem = q8_smem_bytes(D, p.heads_per_cta, p.stages, p.a.num_kv_heads);
   if (smem > (size_t)kQ8SmemLimit) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8SmemLimit);
   if (e != cudaSuccess) return e;
@@ -1134,9 +1071,9 @@ cudaError_t launch_portable_t(const StepArgs& a, const Q8Cache& c, cudaStream_t 
 
 }  // namespace
 
-size_t q8_smem_bytes(int D, int HB, int KW, int NB, int stages, int Hkv) {
+size_t q8_smem_bytes(int D, int HB, int stages, int Hkv) {
   return 1024 /* alignment slack */ + (size_t)stages * (2 * HB * kKB * D + 2 * kKB * Hkv) +
-         (size_t)(KW - 1) * HB * (6 + D / 4) * NB * 128 /* exchange slots */ + sizeof(Q8Smem);
+         sizeof(Q8Smem);
 }
 
 cudaError_t launch_q8_split(const Q8Args& p, int column_blocks, cudaStream_t stream) {

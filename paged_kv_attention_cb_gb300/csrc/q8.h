@@ -46,7 +46,8 @@ struct Q8CtaStart {
   int u;     // global index of the CTA's first key block
   int r;     // its request
   int tile;  // its token tile within the request
-  int u0;    // global index of that item's first key block
+  int item;  // index of that (request, tile) among the step's
+  int u0;    // global index of the item's first key block
   int t0, q_len, seq;  // the request's first query row, query tokens and KV length
 };
 
@@ -66,15 +67,14 @@ struct Q8Args {
   const void* k_new;  // [T, Hkv, D]
   const void* v_new;
   const int64_t* slot_mapping;
-  float* part_o;      // [slot * TT + token][Hq][D]: CTA b's first piece has slot 2 b, its last
-                      // 2 b + 1 (an item between them lies in the CTA and is written directly)
-  float2* part_ml;    // [slot * TT + token][Hq]
+  float* part_o;      // [((item + CTA) * KW + key warp) * TT + token][Hq][D]
+  float2* part_ml;    // the same rows x [Hq]
   Q8CtaStart start[kQ8TableCtas + 1];
 };
 
 // Column blocks (of 8 columns) a CTA's items have: 1, 2 or 4; fp32 queries at most 2.
 cudaError_t launch_q8_split(const Q8Args& p, int column_blocks, cudaStream_t stream);
-size_t q8_smem_bytes(int D, int HB, int KW, int NB, int stages, int Hkv);
+size_t q8_smem_bytes(int D, int HB, int stages, int Hkv);
 
 // One warp per (row, KV head) on the CUDA cores: every shape, no split.
 cudaError_t launch_q8_portable(const StepArgs& a, const Q8Cache& c, cudaStream_t stream);

@@ -32,21 +32,35 @@ int heads_per_cta(int Hkv) {
   return hb;
 }
 
+// Warps per KV head of a split kernel's CTA: as many as the registers of its column blocks allow
+// (16 consumer warps of 96, or 8 of 168), so that few heads still fill the SM.
+int key_warps(int HB, int column_blocks) {
+  int kw = 1;
+  while (kw < 8 && 2 * kw * HB <= (column_blocks == 1 ? 16 : 8)) kw *= 2;
+  return kw;
+}
+
+int tokens_per_tile(int G, int column_blocks) { return std::max(1, 8 * column_blocks / G); }
+
 // Workspace: header (as cb_paged_attention's), statistics and outputs of the partial rows, then
 // the scratch of the prefilled requests (page table, K pages, V pages), whose sizes follow from
-// each step's lengths. The partial rows: two pieces per CTA of up to kMaxColumns / G tokens.
+// each step's lengths.
 struct Layout {
   size_t part_ml, part_o, scratch;
 };
 
-Layout layout_of(int Hkv, int D) {
-  // rows x Hq = 2 C (kMaxColumns / G) Hkv G, with C head groups' worth of at most kQ8TableCtas
-  const size_t entries = (size_t)2 * cb::kQ8TableCtas * kMaxColumns * heads_per_cta(Hkv) *
-                         std::max(1, Hkv / heads_per_cta(Hkv) / cb::kQ8TableCtas + 1);
+Layout layout_of(int64_t R, int64_t T, int Hq, int Hkv, int D) {
+  const int G = std::max(1, Hq / Hkv), HB = heads_per_cta(Hkv);
+  const int64_t C = std::max(1, cb::kQ8TableCtas / (Hkv / HB));
+  int64_t rows = 0;  // (items + CTAs) x warps per head x tokens per item
+  for (int nb = 1; nb <= 4; nb *= 2) {
+    const int64_t TT = tokens_per_tile(G, nb);
+    rows = std::max(rows, ((T + R * (TT - 1)) / TT + R + C) * TT * key_warps(HB, nb));
+  }
   Layout w;
   w.part_ml = cb::kWorkspaceHeaderBytes;
-  w.part_o = w.part_ml + align256(entries * 8);
-  w.scratch = w.part_o + align256(entries * D * 4);
+  w.part_o = w.part_ml + align256((size_t)rows * Hq * 8);
+  w.scratch = w.part_o + align256((size_t)rows * Hq * D * 4);
   return w;
 }
 
@@ -68,7 +82,7 @@ int first_key(int pos0, int window) { return window > 0 ? std::max(0, pos0 - win
 
 // The split kernel's launch over the requests with 1 <= q_len <= max_q.
 void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int max_q,
-                const int32_t* qsl, const int32_t* seq_lens, uint8_t* ws) {
+                const int32_t* qsl, const int32_t* seq_lens, const Layout& w, uint8_t* ws) {
   const int G = a.num_q_heads / a.num_kv_heads;
   int longest = 0;
   for (int r = 0; r < a.num_requests; ++r) {
@@ -87,20 +101,17 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
   p.a = a;
   p.c = c;
   p.max_q = max_q;
-  p.tile_tokens = 8 * nb / G;
+  p.tile_tokens = tokens_per_tile(G, nb);
   p.lg_group = 0;
   while ((1 << p.lg_group) < G) ++p.lg_group;
   const int HB = p.heads_per_cta = heads_per_cta(a.num_kv_heads);
-  // warps per head: as many as the register budget of the column blocks allows (16 consumer
-  // warps of 120 registers, or 8 of 224), so that few heads still fill the SM
-  p.key_warps = 1;
-  while (p.key_warps < 8 && 2 * p.key_warps * HB <= (nb == 1 ? 16 : 8)) p.key_warps *= 2;
-  const size_t fixed = cb::q8_smem_bytes(a.head_dim, HB, p.key_warps, nb, 0, a.num_kv_heads);
-  const size_t per = cb::q8_smem_bytes(a.head_dim, HB, p.key_warps, nb, 1, a.num_kv_heads) - fixed;
+  p.key_warps = key_warps(HB, nb);
+  const size_t fixed = cb::q8_smem_bytes(a.head_dim, HB, 0, a.num_kv_heads);
+  const size_t per = cb::q8_smem_bytes(a.head_dim, HB, 1, a.num_kv_heads) - fixed;
   p.stages = (int)std::min({(size_t)cb::kQ8MaxStages, (cb::kQ8SmemLimit - fixed) / per, cb::kQ8RingBytes / per});
   p.stages -= p.stages % p.key_warps;
 
-  const int TT = p.tile_tokens, W = a.sliding_window;
+  const int TT = p.tile_tokens, KW = p.key_warps, W = a.sliding_window;
   auto blocks = [&](int pos0, int ntok) {
     return (pos0 + ntok - 1) / cb::kQ8KeyBlock - first_key(pos0, W) / cb::kQ8KeyBlock + 1;
   };
@@ -118,28 +129,28 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
   C = std::min(C, (U + cb::kQ8MinBlocksPerCta - 1) / cb::kQ8MinBlocksPerCta);
   p.num_ctas = (int)C;
 
-  // where each CTA's range starts, and the items that several CTAs share
+  // where each CTA's range starts, and the pieces of the rows
   auto start_of = [&](long long b) { return b * U / C; };
   long long u = 0;
-  int b = 0;
+  int b = 0, item = 0;
   each_item([&](int r, int tile, int pos0, int ntok) {
     const int n = blocks(pos0, ntok);
-    for (; b < C && start_of(b) < u + n; ++b) p.start[b] = cb::Q8CtaStart{(int)start_of(b), r, tile, (int)u, qsl[r], qsl[r + 1] - qsl[r], seq_lens[r]};
+    for (; b < C && start_of(b) < u + n; ++b)
+      p.start[b] = cb::Q8CtaStart{(int)start_of(b), r, tile, item, (int)u, qsl[r], qsl[r + 1] - qsl[r], seq_lens[r]};
     const int b0 = (int)(((u + 1) * C + U - 1) / U) - 1;
     const int b1 = (int)(((u + n) * C + U - 1) / U) - 1;
-    if (b1 > b0) {
-      const int slot0 = 2 * b0 + (u > start_of(b0) ? 1 : 0);
+    const int pieces = (b1 - b0 + 1) * KW;
+    if (pieces > 1) {
       for (int i = 0; i < ntok; ++i)
-        plan.merge.push_back(cb::MergeRow{qsl[r] + tile * TT + i, slot0 * TT + i, 0, 1,
-                                          2 * (b0 + 1) * TT + i, 2 * TT, b1 - b0});
-      plan.max_pieces = std::max(plan.max_pieces, b1 - b0 + 1);
+        plan.merge.push_back(cb::MergeRow{qsl[r] + tile * TT + i, (item + b0) * KW * TT + i, TT, pieces, 0, 0, 0});
+      plan.max_pieces = std::max(plan.max_pieces, pieces);
     }
     u += n;
+    ++item;
   });
-  p.start[C] = cb::Q8CtaStart{(int)U, -1, 0, 0, 0, 0, 0};
+  p.start[C] = cb::Q8CtaStart{(int)U, -1, 0, 0, 0, 0, 0, 0};
   p.k_new = p.v_new = nullptr;
   p.slot_mapping = nullptr;
-  const Layout w = layout_of(a.num_kv_heads, a.head_dim);
   p.part_ml = reinterpret_cast<float2*>(ws + w.part_ml);
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
 }
@@ -166,14 +177,13 @@ size_t plan_chunks(Q8Plan& plan, const cb::StepArgs& a, int max_q, const int32_t
 
 // The prefilled requests, up to kPrefillMaxEntries a launch: their pages as bf16, then the tiles.
 cudaError_t run_chunks(const Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c,
-                       uint8_t* ws, cudaStream_t s) {
+                       uint8_t* scratch, cudaStream_t s) {
   int64_t table = 0, total = 0;
   for (const cb::PrefillEntry& e : plan.chunks) {
     const int64_t all = ((int64_t)e.seq_len + a.block_size - 1) / a.block_size;
     table += all;
     total += all - first_key(e.seq_len - e.q_len, a.sliding_window) / 128 * 128 / a.block_size;
   }
-  uint8_t* scratch = ws + layout_of(a.num_kv_heads, a.head_dim).scratch;
   uint8_t* k = scratch + align256((size_t)table * 4);
   uint8_t* v = k + (size_t)total * a.block_size * a.num_kv_heads * a.head_dim * 2;
   int row = 0, dst = 0;
@@ -202,7 +212,7 @@ cudaError_t run_chunks(const Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Ca
     pa.tile_tokens = 128 / (a.num_q_heads / a.num_kv_heads);
     pa.box_keys = std::min(a.block_size, 128);
     pa.metadata_ready = 1;
-    int* header = reinterpret_cast<int*>(ws);
+    int* header = a.error_word;  // the workspace's first word
     pa.exit_counter = header + cb::kExitCounterOffset / 4;
     pa.unit_counter = header + cb::kUnitCounterOffset / 4;
     pa.scatter_counter = header + cb::kScatterCounterOffset / 4;
@@ -274,7 +284,7 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
                                       num_kv_heads, head_dim, block_table_stride, dtype,
                                       h_query_start_loc, h_seq_lens);
   if (st != CB_OK) return st;
-  const Layout w = layout_of(num_kv_heads, head_dim);
+  const Layout w = layout_of(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim);
   if (!workspace || workspace_bytes < w.scratch)
     return report_error(CB_ERR_WORKSPACE, "workspace missing or smaller than cb_workspace_size_q8()");
   if (!cb::is_aligned16(workspace))
@@ -334,7 +344,7 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
       return report_error(CB_ERR_WORKSPACE,
                           "workspace too small for the step's chunks: chunk_kv_tokens of "
                           "cb_workspace_size_q8() must cover the seq_lens of requests with q_len > 1");
-    plan_split(plan, a, c, max_q, h_query_start_loc, h_seq_lens, ws);
+    plan_split(plan, a, c, max_q, h_query_start_loc, h_seq_lens, w, ws);
   }
   cudaError_t e = cudaSuccess;
   if (k_new && fast && plan.split && plan.decode_only) {
@@ -362,7 +372,7 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
       m.parts = cb::merge_parts(plan.max_pieces);
       e = cb::launch_merge(m, plan.merge.data(), (int)plan.merge.size(), s);
     }
-    if (e == cudaSuccess && !plan.chunks.empty()) e = run_chunks(plan, a, c, ws, s);
+    if (e == cudaSuccess && !plan.chunks.empty()) e = run_chunks(plan, a, c, ws + w.scratch, s);
   }
   if (e != cudaSuccess) return cb::report_cuda_error(e, "8-bit attention launch");
   return CB_OK;
@@ -407,11 +417,10 @@ cb_status cb_read_kv_q8(const void* k_cache, const void* v_cache, const void* k_
 size_t cb_workspace_size_q8(int32_t num_requests, int32_t num_tokens, int32_t num_q_heads,
                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
                             int64_t chunk_kv_tokens) {
-  (void)num_tokens;
-  if (num_requests < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+  if (num_requests < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       block_size <= 0)
     return cb::kWorkspaceHeaderBytes;
-  const size_t fixed = layout_of(num_kv_heads, head_dim).scratch;
+  const size_t fixed = layout_of(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim).scratch;
   if (chunk_kv_tokens <= 0) return fixed;
   // each request's pages are rounded up
   const int64_t pages = chunk_kv_tokens / block_size + std::min<int64_t>(num_requests, chunk_kv_tokens);
