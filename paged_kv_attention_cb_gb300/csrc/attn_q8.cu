@@ -17,8 +17,10 @@
 //   request order and CTA b of C takes blocks [b U / C, (b + 1) U / C): equal bytes per CTA.
 //   Each warp's share of an item in a CTA (a piece) becomes a partial row that the merge kernel
 //   joins (merge.h); only an item that one warp per head has to itself is written directly.
-// * Staging. A producer warp brings each block (16 keys, up to 8 KV heads, K and V) with two
-//   swizzled tensor copies and its scales with two bulk copies into a ring of stages.
+// * Staging. Producer warps bring each block (16 keys, up to 8 KV heads, K and V) with two
+//   swizzled tensor copies and its scales with two bulk copies into a ring of stages. Four of
+//   them, taking the blocks in turn: one warp needs ~0.5 us to place and issue a block, which
+//   bounded everything but the widest rows (64 x 32768 with one KV head: 1.2 TB/s).
 // * Operands. e4m3 is exact in fp16, so the contractions are fp16 mma.sync with fp32
 //   accumulation, and the conversion is one instruction per pair (cvt.f16x2.e4m3x2). q is
 //   scaled per row by a power of two to a largest magnitude in [2^13, 2^14): a bf16 row is
@@ -39,7 +41,9 @@
 // * Warps. KW warps share a KV head and take the blocks in turn, each with its own state and its
 //   own partial rows: a join through shared memory at the end of each piece cost 1.5 us there,
 //   in which the stream stood still, and the merge kernel has to run anyway. At 8 heads and two
-//   warps each, one warp has ~1400 cycles per 16-key block at the HBM rate.
+//   warps each, one warp has ~1400 cycles per 16-key block at the HBM rate. Runs of query tokens
+//   have up to 64 columns: CW warps of a head then read the same blocks for 16 columns each (the
+//   CTA has that many fewer heads), so that the cache is still read once.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <float.h>
@@ -210,7 +214,7 @@ CB_DEV int blocks_of(int pos0, int ntok, int window) {
 
 // NB column blocks of 8; F32: fp32 queries and outputs (operands split into two fp16 parts).
 template <int D, int NB, bool F32>
-__global__ void __launch_bounds__((NB == 1 ? 16 : 8) * 32 + 32, 1)
+__global__ void __launch_bounds__(((NB == 1 ? 16 : 8) + kQ8Producers) * 32, 1)
 q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ Q8Args p) {
   constexpr int kKS = D / 16;          // contraction steps over head_dim; output tiles of 16
@@ -218,7 +222,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
   extern __shared__ __align__(1024) uint8_t smem_dyn[];
   uint8_t* base = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~uintptr_t(1023));
-  const int HB = p.heads_per_cta, KW = p.key_warps, Hkv = p.a.num_kv_heads;
+  const int HB = p.heads_per_cta, KW = p.key_warps, CW = p.column_warps, Hkv = p.a.num_kv_heads;
   const int box_bytes = HB * kKB * D;      // K (or V) of one block
   const int stage_bytes = 2 * box_bytes;
   const int scale_bytes = kKB * Hkv;       // K (or V) scales of one block, every head
@@ -230,14 +234,14 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.x;
   const int hg = blockIdx.y;
-  const int nwarps = HB * KW;  // consumer warps; the next one is the producer
+  const int nwarps = HB * KW * CW;  // consumer warps; the producers follow
   const int W = p.a.sliding_window;
   const int TT = p.tile_tokens;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&sm.full[s], 1);
-      mbar_init(&sm.empty[s], HB);
+      mbar_init(&sm.empty[s], HB * CW);
     }
     for (int s = 0; s < kQueue; ++s) {
       mbar_init(&sm.pfull[s], 1);
@@ -258,9 +262,12 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
   allow_dependent_launch();
   __syncthreads();
 
-  int issued_blocks = 0;  // producer: copies issued (for the drain)
-  if (warp == nwarps) {
-    // =================================================== producer warp
+  const int producer = warp - nwarps;
+  int issued_blocks = 0;  // producers: one past the last block whose copies this warp issued
+  if (producer >= 0) {
+    // =================================================== producer warps
+    // All walk the same pieces; block i is issued by warp i % kQ8Producers, and the first also
+    // hands the pieces to the consumers.
     const int u_lo = p.start[b].u, u_hi = p.start[b + 1].u;
     const uint64_t policy = l2_policy_evict_first();  // the stream is read once
     const int BS = p.a.block_size;
@@ -309,7 +316,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // page ids of key blocks kb .. kb + n - 1 of the request (lane l: block kb + l)
     auto load_pages = [&](int rr, int kb, int n) -> int {
       return lane < n ? __ldg(p.a.block_table + (long long)rr * p.a.bt_stride +
-                              bt_entry((kb + lane) * kKB / BS, p.a.ring_blocks))
+                              ((kb + lane) * kKB >> p.lg_block))
                       : 0;
     };
     bool more = u_lo < u_hi;
@@ -325,45 +332,47 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       pages = load_pages(r, kb0, min(32, kb1 - kb0));
     }
     while (more && ok) {
-      const int qs = k % kQueue;
-      if (k >= kQueue &&
-          !mbar_wait_warp_or_abort(&sm.pempty[qs], (uint32_t)(k / kQueue - 1) & 1, &sm.abort_flag)) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        Q8Piece& d = sm.piece[qs];
-        d.r = r;
-        d.t0 = t0 + tile * TT;
-        d.ntok = ntok;
-        d.n = kb1 - kb0;
-        d.kb0 = kb0;
-        d.pos0 = pos0;
-        d.slot = item + b;
-        d.direct = KW == 1 && u0 >= u_lo && u0 + nblk <= u_hi;
-        d.last = kb1 == kb_lo + nblk;
-        mbar_arrive(&sm.pfull[qs]);
-      }
-      __syncwarp();
-      ++k;
-      {
-        // the piece's query rows and new rows on their way into L1: under a full stream a load
-        // takes over a microsecond, which the consumers would wait for at every piece
-        const int elt = F32 ? 4 : 2, t = t0 + tile * TT;
-        const uint8_t* q = static_cast<const uint8_t*>(p.a.q);
-        const int row = p.a.num_q_heads * D * elt, part = (HB << p.lg_group) * D * elt;
-        for (int i = lane * 128; i < ntok * part; i += 32 * 128)
-          prefetch_l1(q + (long long)(t + i / part) * row + hg * part + i % part);
-        if (p.k_new != nullptr && kb1 == kb_lo + nblk) {
-          const long long at = ((long long)t * Hkv + hg * HB) * D * elt;
-          for (int i = lane * 128; i < HB * D * elt; i += 32 * 128) {
-            prefetch_l1(static_cast<const uint8_t*>(p.k_new) + at + i);
-            prefetch_l1(static_cast<const uint8_t*>(p.v_new) + at + i);
+      if (producer == 0) {
+        const int qs = k % kQueue;
+        if (k >= kQueue &&
+            !mbar_wait_warp_or_abort(&sm.pempty[qs], (uint32_t)(k / kQueue - 1) & 1, &sm.abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          Q8Piece& d = sm.piece[qs];
+          d.r = r;
+          d.t0 = t0 + tile * TT;
+          d.ntok = ntok;
+          d.n = kb1 - kb0;
+          d.kb0 = kb0;
+          d.pos0 = pos0;
+          d.slot = item + b;
+          d.direct = KW == 1 && u0 >= u_lo && u0 + nblk <= u_hi;
+          d.last = kb1 == kb_lo + nblk;
+          mbar_arrive(&sm.pfull[qs]);
+        }
+        __syncwarp();
+        {
+          // the piece's query rows and new rows on their way into L1: under a full stream a load
+          // takes over a microsecond, which the consumers would wait for at every piece
+          const int elt = F32 ? 4 : 2, t = t0 + tile * TT;
+          const uint8_t* q = static_cast<const uint8_t*>(p.a.q);
+          const int row = p.a.num_q_heads * D * elt, part = (HB << p.lg_group) * D * elt;
+          for (int i = lane * 128; i < ntok * part; i += 32 * 128)
+            prefetch_l1(q + (long long)(t + i / part) * row + hg * part + i % part);
+          if (p.k_new != nullptr && kb1 == kb_lo + nblk) {
+            const long long at = ((long long)t * Hkv + hg * HB) * D * elt;
+            for (int i = lane * 128; i < HB * D * elt; i += 32 * 128) {
+              prefetch_l1(static_cast<const uint8_t*>(p.k_new) + at + i);
+              prefetch_l1(static_cast<const uint8_t*>(p.v_new) + at + i);
+            }
+            if (lane == 0) prefetch_l1(p.slot_mapping + t);
+            if (lane == 1) prefetch_l1(p.a.block_table + (long long)r * p.a.bt_stride + pos0 / BS);
           }
-          if (lane == 0) prefetch_l1(p.slot_mapping + t);
-          if (lane == 1) prefetch_l1(p.a.block_table + (long long)r * p.a.bt_stride + pos0 / BS);
         }
       }
+      ++k;
       // the item after this one, looked up once this piece's first copy is out
       bool looked = false;
       int nr = r, n_kb0 = 0, n_kb1 = 0;
@@ -373,33 +382,33 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const int n = min(32, last - kb_base);
         const int cur = pages;
         for (int j = 0; j < n; ++j) {
-          const int pg = __shfl_sync(0xffffffffu, cur, j);
-          if (round > 0 && !mbar_wait_warp_or_abort(&sm.empty[s], (uint32_t)(round - 1) & 1,
-                                                    &sm.abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (*reinterpret_cast<volatile int*>(&sm.abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            const int key0 = ((kb_base + j) * kKB) % BS;
-            uint8_t* st = stages + s * stage_bytes;
-            uint8_t* sc = scales + s * 2 * scale_bytes;
-            const bool page_ok = pg >= 0 && pg < p.a.num_blocks;
-            if (!page_ok) record_error(p.a.error_word, CB_DEVERR_BLOCK_ID);
-            mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(stage_bytes + (page_ok ? 2 * scale_bytes : 0)));
-            const int page = page_ok ? pg : p.a.num_blocks;  // past the pool: zeros
-            tma_load_4d_hint(st, &tmap_k, &sm.full[s], 0, key0, hg * HB, page, policy);
-            tma_load_4d_hint(st + box_bytes, &tmap_v, &sm.full[s], 0, key0, hg * HB, page, policy);
-            if (page_ok) {
-              const long long at = ((long long)pg * BS + key0) * Hkv;
-              bulk_load(sc, p.c.k_scale + at, (uint32_t)scale_bytes, &sm.full[s]);
-              bulk_load(sc + scale_bytes, p.c.v_scale + at, (uint32_t)scale_bytes, &sm.full[s]);
+          if (i % kQ8Producers == producer) {
+            const int pg = __shfl_sync(0xffffffffu, cur, j);
+            if ((round > 0 &&
+                 !mbar_wait_warp_or_abort(&sm.empty[s], (uint32_t)(round - 1) & 1, &sm.abort_flag)) ||
+                *reinterpret_cast<volatile int*>(&sm.abort_flag)) {
+              ok = false;
+              break;
             }
+            if (lane == 0) {
+              const int key0 = ((kb_base + j) * kKB) & (BS - 1);
+              uint8_t* st = stages + s * stage_bytes;
+              uint8_t* sc = scales + s * 2 * scale_bytes;
+              const bool page_ok = pg >= 0 && pg < p.a.num_blocks;
+              if (!page_ok) record_error(p.a.error_word, CB_DEVERR_BLOCK_ID);
+              mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(stage_bytes + (page_ok ? 2 * scale_bytes : 0)));
+              const int page = page_ok ? pg : p.a.num_blocks;  // past the pool: zeros
+              tma_load_4d_hint(st, &tmap_k, &sm.full[s], 0, key0, hg * HB, page, policy);
+              tma_load_4d_hint(st + box_bytes, &tmap_v, &sm.full[s], 0, key0, hg * HB, page, policy);
+              if (page_ok) {
+                const long long at = (((long long)pg << p.lg_block) + key0) * Hkv;
+                bulk_load(sc, p.c.k_scale + at, (uint32_t)scale_bytes, &sm.full[s]);
+                bulk_load(sc + scale_bytes, p.c.v_scale + at, (uint32_t)scale_bytes, &sm.full[s]);
+              }
+            }
+            __syncwarp();
+            issued_blocks = i + 1;
           }
-          __syncwarp();
           ++i;
           if (++s == p.stages) {
             s = 0;
@@ -440,7 +449,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       kb0 = n_kb0;
       kb1 = n_kb1;
     }
-    if (ok) {
+    if (ok && producer == 0) {
       const int qs = k % kQueue;
       if (k >= kQueue &&
           !mbar_wait_warp_or_abort(&sm.pempty[qs], (uint32_t)(k / kQueue - 1) & 1, &sm.abort_flag))
@@ -454,8 +463,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       record_error(p.a.error_word, CB_DEVERR_TIMEOUT);
       set_abort(&sm.abort_flag);
     }
-    issued_blocks = i;
-  } else if (warp < nwarps) {
+  } else {
     // =================================================== consumer warps
     auto give_up = [&]() {
       if (lane == 0) {
@@ -464,7 +472,8 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       }
     };
     auto consume = [&]() {
-      const int hl = warp % HB, kw = warp / HB;
+      const int hl = warp % HB, kw = warp / HB % KW;
+      const int col0 = warp / (HB * KW) * 8 * NB;  // this warp's columns of the item
       const int gid = lane >> 2, tq = lane & 3;
       const int G = 1 << p.lg_group;
       const int head = hg * HB + hl;  // KV head
@@ -550,7 +559,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
         float cs0[NB], cs1[NB];  // score factors of columns 8 nb + 2 tq, + 1
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const int col = 8 * nb + gid;
+          const int col = col0 + 8 * nb + gid;
           const int tok = col >> p.lg_group;
           const bool live = tok < d.ntok;
           const long long at =
@@ -693,8 +702,8 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
             float s2 = sa[nb][2] * cs0[nb] * fb, s3 = sa[nb][3] * cs1[nb] * fb;
             float t0 = s0 + ea, t1 = s1 + ea, t2 = s2 + eb, t3 = s3 + eb;
             if (edge) {  // both: a slot that is not attended may hold any scale
-              const int h0 = d.pos0 + ((8 * nb + 2 * tq) >> p.lg_group);
-              const int h1 = d.pos0 + ((8 * nb + 2 * tq + 1) >> p.lg_group);
+              const int h0 = d.pos0 + ((col0 + 8 * nb + 2 * tq) >> p.lg_group);
+              const int h1 = d.pos0 + ((col0 + 8 * nb + 2 * tq + 1) >> p.lg_group);
               const int l0 = first_key(h0, W), l1 = first_key(h1, W);
               if (ka < l0 || ka > h0) s0 = t0 = -INFINITY;
               if (ka < l1 || ka > h1) s1 = t1 = -INFINITY;
@@ -787,8 +796,8 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
               uint32_t at[NB][2];
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
-                const int h0 = d.pos0 + ((8 * nb + 2 * tq) >> p.lg_group);
-                const int h1 = d.pos0 + ((8 * nb + 2 * tq + 1) >> p.lg_group);
+                const int h0 = d.pos0 + ((col0 + 8 * nb + 2 * tq) >> p.lg_group);
+                const int h1 = d.pos0 + ((col0 + 8 * nb + 2 * tq + 1) >> p.lg_group);
                 const int l0 = first_key(h0, W), l1 = first_key(h1, W);
                 const float a0 = ka >= l0 && ka <= h0 ? 1.f : 0.f, a1 = ka >= l1 && ka <= h1 ? 1.f : 0.f;
                 const float b0 = kb >= l0 && kb <= h0 ? 1.f : 0.f, b1 = kb >= l1 && kb <= h1 ? 1.f : 0.f;
@@ -857,7 +866,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
         for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int col = 8 * nb + 2 * tq + c;
+            const int col = col0 + 8 * nb + 2 * tq + c;
             const int tok = col >> p.lg_group;
             if (tok >= d.ntok) continue;
             const int h = head * G + (col & (G - 1));
@@ -902,9 +911,9 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
   // As in the bf16 decode kernel: after a wait that gave up, the latest copy of each stage may
   // be in flight; it is waited for before the shared memory is released.
   __syncthreads();
-  if (warp == nwarps && lane == 0 && *reinterpret_cast<volatile int*>(&sm.abort_flag)) {
-    const int first = issued_blocks > p.stages ? issued_blocks - p.stages : 0;
-    for (int j = first; j < issued_blocks; ++j)
+  // (Each producer waits for its own blocks among the latest of every stage that it knows of.)
+  if (producer >= 0 && lane == 0 && *reinterpret_cast<volatile int*>(&sm.abort_flag)) {
+    for (int j = issued_blocks - 1; j >= 0 && j >= issued_blocks - p.stages; j -= kQ8Producers)
       mbar_wait(&sm.full[j % p.stages], (uint32_t)(j / p.stages) & 1);
   }
 }
@@ -1039,7 +1048,8 @@ cudaError_t launch_split_t(const Q8Args& p, cudaStream_t s) {
   if (e == cudaSuccess) e = cache_map(&mv, p.c.v, p.a, p.heads_per_cta);
   if (e != cudaSuccess) return e;
   return launch_pdl(kDecodeQ8, kern, dim3(p.num_ctas, p.a.num_kv_heads / p.heads_per_cta),
-                    dim3(p.heads_per_cta * p.key_warps * 32 + 32), smem, s, mk, mv, p);
+                    dim3((p.heads_per_cta * p.key_warps * p.column_warps + kQ8Producers) * 32), smem, s,
+                    mk, mv, p);
 }
 
 template <int D>
@@ -1050,7 +1060,6 @@ cudaError_t launch_split_d(const Q8Args& p, int nb, cudaStream_t s) {
   } else {
     if (nb == 1) return launch_split_t<D, 1, false>(p, s);
     if (nb == 2) return launch_split_t<D, 2, false>(p, s);
-    if (nb == 4) return launch_split_t<D, 4, false>(p, s);
   }
   return cudaErrorInvalidValue;
 }

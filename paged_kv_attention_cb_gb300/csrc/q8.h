@@ -33,6 +33,8 @@ cudaError_t launch_read_kv_q8(void* k_out, void* v_out, const Q8Cache& c,
 constexpr int kQ8KeyBlock = 16;      // keys per unit of work (and per stage of the ring)
 constexpr int kQ8MaxStages = 32;
 constexpr int kQ8MaxHeads = 8;       // KV heads per CTA
+constexpr int kQ8Producers = 4;      // producer warps per CTA
+constexpr int kQ8MaxColumnWarps = 4; // warps of a head on different columns
 constexpr int kQ8TableCtas = 192;    // CTAs per group of heads (their starts are arguments)
 constexpr int kQ8SmemLimit = 232448; // 227 KiB dynamic shared memory per CTA
 // Bytes of the ring: a little over the latency times the rate of one SM's share of HBM. More
@@ -56,9 +58,11 @@ struct Q8Args {
   Q8Cache c;
   int num_ctas;       // CTA b takes the key blocks from start[b].u to start[b + 1].u
   int heads_per_cta;  // HB
-  int key_warps;      // KW: warps per KV head; block i goes to warp i % KW
-  int stages;         // multiple of KW
-  int tile_tokens;    // TT: query tokens per item (TT * G columns, at most 8 NB)
+  int key_warps;      // KW: warps per KV head and columns; block i goes to those with i % KW
+  int column_warps;   // CW: warps per KV head and block, each with 8 NB of the item's columns
+  int stages;         // multiple of KW and of kQ8Producers
+  int tile_tokens;    // TT: query tokens per item (TT * G columns, at most 8 NB CW)
+  int lg_block;       // log2 of block_size
   int lg_group;       // log2 of query heads per KV head
   int max_q;
   // Steps of decode rows only: the warp that reads a request's last key block quantises the
@@ -72,7 +76,7 @@ struct Q8Args {
   Q8CtaStart start[kQ8TableCtas + 1];
 };
 
-// Column blocks (of 8 columns) a CTA's items have: 1, 2 or 4; fp32 queries at most 2.
+// Column blocks (of 8 columns) per warp: 1 or 2.
 cudaError_t launch_q8_split(const Q8Args& p, int column_blocks, cudaStream_t stream);
 size_t q8_smem_bytes(int D, int HB, int stages, int Hkv);
 

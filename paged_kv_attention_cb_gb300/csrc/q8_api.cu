@@ -22,25 +22,32 @@ constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Requests of more query columns (tokens x grouped heads) than this are prefilled: their pages
 // are turned into bf16 once and the tcgen05 tiles read those. Below it the split kernel reads
-// the 8-bit pages directly, once per 32 columns.
+// the 8-bit pages directly, once per 64 columns.
 constexpr int kChunkColumns = 64;
-constexpr int kMaxColumns = 32;  // columns of a split kernel's item at most
 
-int heads_per_cta(int Hkv) {
-  int hb = std::min(Hkv, cb::kQ8MaxHeads);
-  while (Hkv % hb != 0) --hb;
-  return hb;
+// How a CTA's consumer warps divide the work on items of up to `columns` query columns: 16 warps
+// of 96 registers with 8 columns each, or 8 of 168 with 16.
+struct Split {
+  int column_blocks;  // NB: 8-column blocks per warp
+  int column_warps;   // CW
+  int heads;          // HB: KV heads per CTA, a divisor of Hkv
+  int key_warps;      // KW
+};
+
+Split split_of(int64_t columns, int Hkv) {
+  Split s;
+  s.column_blocks = columns <= 8 ? 1 : 2;
+  s.column_warps = 1;
+  while (s.column_warps < cb::kQ8MaxColumnWarps && 16 * s.column_warps < columns) s.column_warps *= 2;
+  const int warps = s.column_blocks == 1 ? 16 : 8;
+  s.heads = std::min({Hkv, cb::kQ8MaxHeads, warps / s.column_warps});
+  while (Hkv % s.heads != 0) --s.heads;
+  s.key_warps = 1;
+  while (s.key_warps < 8 && 2 * s.key_warps * s.heads * s.column_warps <= warps) s.key_warps *= 2;
+  return s;
 }
 
-// Warps per KV head of a split kernel's CTA: as many as the registers of its column blocks allow
-// (16 consumer warps of 96, or 8 of 168), so that few heads still fill the SM.
-int key_warps(int HB, int column_blocks) {
-  int kw = 1;
-  while (kw < 8 && 2 * kw * HB <= (column_blocks == 1 ? 16 : 8)) kw *= 2;
-  return kw;
-}
-
-int tokens_per_tile(int G, int column_blocks) { return std::max(1, 8 * column_blocks / G); }
+int tokens_per_item(const Split& s, int G) { return 8 * s.column_blocks * s.column_warps / G; }
 
 // Workspace: header (as cb_paged_attention's), statistics and outputs of the partial rows, then
 // the scratch of the prefilled requests (page table, K pages, V pages), whose sizes follow from
@@ -50,12 +57,13 @@ struct Layout {
 };
 
 Layout layout_of(int64_t R, int64_t T, int Hq, int Hkv, int D) {
-  const int G = std::max(1, Hq / Hkv), HB = heads_per_cta(Hkv);
-  const int64_t C = std::max(1, cb::kQ8TableCtas / (Hkv / HB));
+  const int G = std::max(1, Hq / Hkv);
   int64_t rows = 0;  // (items + CTAs) x warps per head x tokens per item
-  for (int nb = 1; nb <= 4; nb *= 2) {
-    const int64_t TT = tokens_per_tile(G, nb);
-    rows = std::max(rows, ((T + R * (TT - 1)) / TT + R + C) * TT * key_warps(HB, nb));
+  for (int columns = std::max(8, G); columns <= 16 * cb::kQ8MaxColumnWarps; columns *= 2) {
+    const Split s = split_of(columns, Hkv);
+    const int64_t TT = std::max(1, tokens_per_item(s, G));
+    const int64_t C = std::max(1, cb::kQ8TableCtas / (Hkv / s.heads));
+    rows = std::max(rows, ((T + R * (TT - 1)) / TT + R + C) * TT * s.key_warps);
   }
   Layout w;
   w.part_ml = cb::kWorkspaceHeaderBytes;
@@ -92,24 +100,29 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
   if (longest == 0) return;
   plan.split = true;
   plan.decode_only = longest == 1 && plan.chunks.empty();
-  const int top = a.dtype == CB_F32 ? 2 : 4;  // column blocks (fp32 queries: twice the operands)
-  int nb = 1;
-  while (nb < top && 8 * nb < std::min<int64_t>((int64_t)longest * G, kMaxColumns)) nb *= 2;
-  plan.column_blocks = nb;
+  const Split sp = split_of((int64_t)longest * G, a.num_kv_heads);
+  plan.column_blocks = sp.column_blocks;
 
   cb::Q8Args& p = plan.args;
   p.a = a;
   p.c = c;
   p.max_q = max_q;
-  p.tile_tokens = tokens_per_tile(G, nb);
+  p.tile_tokens = tokens_per_item(sp, G);
   p.lg_group = 0;
   while ((1 << p.lg_group) < G) ++p.lg_group;
-  const int HB = p.heads_per_cta = heads_per_cta(a.num_kv_heads);
-  p.key_warps = key_warps(HB, nb);
+  p.lg_block = 0;
+  while ((1 << p.lg_block) < a.block_size) ++p.lg_block;
+  const int HB = p.heads_per_cta = sp.heads;
+  p.column_warps = sp.column_warps;
+  p.key_warps = sp.key_warps;
   const size_t fixed = cb::q8_smem_bytes(a.head_dim, HB, 0, a.num_kv_heads);
   const size_t per = cb::q8_smem_bytes(a.head_dim, HB, 1, a.num_kv_heads) - fixed;
-  p.stages = (int)std::min({(size_t)cb::kQ8MaxStages, (cb::kQ8SmemLimit - fixed) / per, cb::kQ8RingBytes / per});
-  p.stages -= p.stages % p.key_warps;
+  // each stage belongs to one producer and one key warp: whole multiples of both counts
+  const int m = std::max(p.key_warps, cb::kQ8Producers);
+  p.stages = (int)std::min<size_t>(cb::kQ8MaxStages, cb::kQ8RingBytes / per) / m * m;
+  if (p.stages * per < cb::kQ8RingBytes * 3 / 4 && p.stages + m <= cb::kQ8MaxStages &&
+      fixed + (p.stages + m) * per <= (size_t)cb::kQ8SmemLimit)
+    p.stages += m;
 
   const int TT = p.tile_tokens, KW = p.key_warps, W = a.sliding_window;
   auto blocks = [&](int pos0, int ntok) {
