@@ -43,7 +43,7 @@ Split split_of(int64_t columns, int Hkv) {
   s.heads = std::min({Hkv, cb::kQ8MaxHeads, warps / s.column_warps});
   while (Hkv % s.heads != 0) --s.heads;
   s.key_warps = 1;
-  while (s.key_warps < 8 && 2 * s.key_warps * s.heads * s.column_warps <= warps) s.key_warps *= 2;
+  while (2 * s.key_warps * s.heads * s.column_warps <= warps) s.key_warps *= 2;
   return s;
 }
 
@@ -76,7 +76,18 @@ size_t scratch_bytes(int64_t table_pages, int64_t pages, int block_size, int Hkv
   return align256((size_t)table_pages * 4) + 2 * (size_t)pages * block_size * Hkv * D * 2;
 }
 
+// A request's query tokens that a CTA's warps take at once, and the key blocks they attend.
+struct Item {
+  int r, tile, blocks;
+};
+
+// What starting and finishing a piece of an item costs a CTA, in key blocks: its query rows, the
+// first maximum, the partial rows (64 requests of 128 .. 2048 positions: CTAs with one piece were
+// done after 23.1 us, with two after 25.9, with three after 28.7; a block takes 0.8).
+constexpr int kPieceBlocks = 3;
+
 struct Q8Plan {
+  std::vector<Item> items;
   bool split = false;
   bool decode_only = false;  // every request has at most one query row
   int column_blocks = 1;
@@ -128,39 +139,72 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
   auto blocks = [&](int pos0, int ntok) {
     return (pos0 + ntok - 1) / cb::kQ8KeyBlock - first_key(pos0, W) / cb::kQ8KeyBlock + 1;
   };
+  std::vector<Item>& items = plan.items;
+  items.clear();
   long long U = 0;
-  auto each_item = [&](auto&& f) {
-    for (int r = 0; r < a.num_requests; ++r) {
-      const int q = qsl[r + 1] - qsl[r];
-      if (q < 1 || q > max_q) continue;
-      for (int i = 0; i * TT < q; ++i) f(r, i, seq_lens[r] - q + i * TT, std::min(TT, q - i * TT));
+  for (int r = 0; r < a.num_requests; ++r) {
+    const int q = qsl[r + 1] - qsl[r];
+    if (q < 1 || q > max_q) continue;
+    for (int i = 0; i * TT < q; ++i) {
+      const int pos0 = seq_lens[r] - q + i * TT, ntok = std::min(TT, q - i * TT);
+      const int n = blocks(pos0, ntok);
+      items.push_back(Item{r, i, n});
+      U += n;
     }
-  };
-  each_item([&](int, int, int pos0, int ntok) { U += blocks(pos0, ntok); });
+  }
   const int groups = a.num_kv_heads / HB;
   long long C = std::max(1, std::min(cb::sm_count(), cb::kQ8TableCtas) / groups);
   C = std::min(C, (U + cb::kQ8MinBlocksPerCta - 1) / cb::kQ8MinBlocksPerCta);
-  p.num_ctas = (int)C;
 
-  // where each CTA's range starts, and the pieces of the rows
-  auto start_of = [&](long long b) { return b * U / C; };
-  long long u = 0;
-  int b = 0, item = 0;
-  each_item([&](int r, int tile, int pos0, int ntok) {
-    const int n = blocks(pos0, ntok);
-    for (; b < C && start_of(b) < u + n; ++b)
-      p.start[b] = cb::Q8CtaStart{(int)start_of(b), r, tile, item, (int)u, qsl[r], qsl[r + 1] - qsl[r], seq_lens[r]};
-    const int b0 = (int)(((u + 1) * C + U - 1) / U) - 1;
-    const int b1 = (int)(((u + n) * C + U - 1) / U) - 1;
-    const int pieces = (b1 - b0 + 1) * KW;
-    if (pieces > 1) {
-      for (int i = 0; i < ntok; ++i)
-        plan.merge.push_back(cb::MergeRow{qsl[r] + tile * TT + i, (item + b0) * KW * TT + i, TT, pieces, 0, 0, 0});
-      plan.max_pieces = std::max(plan.max_pieces, pieces);
+  // ---- the partition: CTAs are filled in order up to a load, the blocks they read and
+  // kPieceBlocks for each piece they have; the least load (to a block) that C CTAs take
+  auto fill = [&](long long load, auto&& piece) -> long long {  // CTAs used
+    long long cta = 0, have = 0;
+    for (size_t i = 0; i < items.size(); ++i) {
+      int at = 0;
+      while (at < items[i].blocks) {
+        if (have + kPieceBlocks + 1 > load && have > 0) {
+          ++cta;
+          have = 0;
+        }
+        const int n = (int)std::min<long long>(items[i].blocks - at, std::max<long long>(1, load - have - kPieceBlocks));
+        piece((int)cta, (int)i, at, n);
+        have += kPieceBlocks + n;
+        at += n;
+      }
+    }
+    return cta + 1;
+  };
+  long long lo = (U + C - 1) / C + kPieceBlocks;  // no less
+  long long hi = lo + (long long)kPieceBlocks * (long long)((items.size() + C - 1) / C + 1);
+  auto nothing = [](int, int, int, int) {};
+  while (fill(hi, nothing) > C) hi += hi - lo + 1;
+  while (lo < hi) {
+    const long long mid = (lo + hi) / 2;
+    if (fill(mid, nothing) <= C) hi = mid; else lo = mid + 1;
+  }
+  int b0 = 0, last_cta = -1, u = 0, u0 = 0;
+  fill(hi, [&](int cta, int i, int at, int n) {
+    const Item& it = items[i];
+    if (at == 0) {
+      b0 = cta;
+      u0 = u;
+    }
+    if (cta != last_cta) {
+      p.start[cta] = cb::Q8CtaStart{u, it.r, it.tile, i, u0, qsl[it.r], qsl[it.r + 1] - qsl[it.r], seq_lens[it.r]};
+      last_cta = cta;
     }
     u += n;
-    ++item;
+    const int pieces = (cta - b0 + 1) * KW;
+    if (at + n == it.blocks && pieces > 1) {
+      const int t0 = qsl[it.r] + it.tile * TT, ntok = std::min(TT, qsl[it.r + 1] - t0);
+      for (int k = 0; k < ntok; ++k)
+        plan.merge.push_back(cb::MergeRow{t0 + k, (i + b0) * KW * TT + k, TT, pieces, 0, 0, 0});
+      plan.max_pieces = std::max(plan.max_pieces, pieces);
+    }
   });
+  C = last_cta + 1;
+  p.num_ctas = (int)C;
   p.start[C] = cb::Q8CtaStart{(int)U, -1, 0, 0, 0, 0, 0, 0};
   p.k_new = p.v_new = nullptr;
   p.slot_mapping = nullptr;
