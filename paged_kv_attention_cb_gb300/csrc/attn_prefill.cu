@@ -246,6 +246,15 @@ CB_DEV void quad_transpose(uint32_t (&w)[32], int lane) {
   }
 }
 
+// Partial row of token `tok` of entry e in a split (t: the group, tok0: the unit's first token;
+// both: a unit of two query tiles).
+CB_DEV long long partial_row(const PrefixArgs& p, int e, int split, int t, bool both, int tok0, int tok) {
+  const int tiles = p.entries[e].n_qtiles, n = p.entries[e].q_len;
+  const int body = tiles & 1 ? (tiles - 1) * p.tile_tokens : n;  // tokens before the tail
+  if (both) return (long long)p.part_row[e] + (long long)split * body + tok;
+  return (long long)p.tail_row[e] + (long long)(2 * split + t) * (n - body) + (tok - tok0);
+}
+
 // The pages of key tile `key_base` in `gen` (bit i: page i of the tile), row by row into
 // the ring slot `dst` (128B-swizzled rows of 64 of head_dim per half): a new position whose
 // slot is its own (bit clear in `bad`) from the step's new rows, any other from its cache
@@ -692,20 +701,43 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
       return mbar_wait_warp_or_abort(&bar.full[i % kStages], (uint32_t)((i / kStages) & 1),
                                      &bar.abort);
     };
+    // Over a shared prefix a unit of one query tile is taken by both groups, each with one half of
+    // every key tile, so that one group's softmax runs beside the other's products as with two
+    // query tiles (one group alone took 1.85 us a key tile, two with a tile each 2.05 us).
+    bool halves = false;
+    constexpr uint32_t idS64 = umma_idesc_bf16(kRows, kKeys / 2, false);
     // S_t = Q_t K^T with K in ring slot i; its completion is signalled on s_full[t]
     auto qk = [&](int t, int i) {
-      const uint64_t dq = dQ + (uint64_t)(t * (kTile >> 4));
-      const uint64_t dk = dK + (uint64_t)((i % kStages) * (kTile >> 4));
+      uint64_t dq = dQ + (uint64_t)(t * (kTile >> 4));
+      uint64_t dk = dK + (uint64_t)((i % kStages) * (kTile >> 4));
+      uint32_t id = idS;
+      if constexpr (kShared) {
+        if (halves) {
+          dq = dQ;
+          dk += (uint64_t)(t * ((kKeys / 2 * 128) >> 4));
+          id = idS64;
+        }
+      }
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
-        umma_bf16_elect(tmem + t * kKeys, dq + off, dk + off, idS, ks > 0 ? 1u : 0u);
+        umma_bf16_elect(tmem + t * kKeys, dq + off, dk + off, id, ks > 0 ? 1u : 0u);
       }
       umma_commit_elect(&bar.s_full[t]);
     };
-    // O_t += P_t V with P in the first 64 columns of S_t and V in ring slot i
+    // O_t += P_t V with P in the first columns of S_t and V in ring slot i
     auto pv = [&](int t, int i, bool acc) {
       const uint64_t dv = dV + (uint64_t)((i % kStages) * (kTile >> 4));
+      if constexpr (kShared) {
+        if (halves) {
+#pragma unroll
+          for (int ks = 0; ks < kKeys / 32; ++ks)
+            umma_bf16_tmem_a_elect(tmem + 2 * kKeys + t * D, tmem + t * kKeys + ks * 8,
+                                   dv + (uint64_t)((t * (kKeys / 32) + ks) * (2048 >> 4)), idO,
+                                   (acc || ks > 0) ? 1u : 0u);
+          return;
+        }
+      }
 #pragma unroll
       for (int ks = 0; ks < kKeys / 16; ++ks)
         umma_bf16_tmem_a_elect(tmem + 2 * kKeys + t * D, tmem + t * kKeys + ks * 8,
@@ -723,7 +755,8 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
       if (!d.live) break;
       const Geo e = unit_geo(d);
       const int nkt = e.nkt;
-      const bool has_b = e.has_b;
+      if constexpr (kShared) halves = !e.has_b;
+      const bool has_b = e.has_b || halves;  // group B has work
       ok = mbar_wait_warp_or_abort(&bar.q_full, (uint32_t)(u & 1), &bar.abort) && slot_ready(i_base);
       if (!ok) break;
       tcgen05_fence_after();
@@ -818,10 +851,12 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         break;
       }
       int kt0, nkt, seq, min_kv, max_kv, tile_max_kv_min, tile_min_kv_max;
+      bool both = true;  // the unit has two query tiles (else, over a shared prefix: this group has
+                         // one half of every key tile)
       {
         const Geo e = CB_UNIT_GEO();
         const int unit_nkt = e.nkt;
-        const bool tile_live = t == 0 || e.has_b;
+        const bool tile_live = t == 0 || e.has_b || kShared;
         if (!tile_live) {  // this unit has no tile B
           i_base += 2 * unit_nkt;
           CB_RELEASE_UNIT();
@@ -830,7 +865,8 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         kt0 = e.kt0;
         nkt = e.nkt;
         seq = e.seq;
-        const int tok0 = (e.qt0 + t) * TQ;
+        if constexpr (kShared) both = e.has_b;
+        const int tok0 = (e.qt0 + (kShared && !e.has_b ? 0 : t)) * TQ;
         const int qpos = e.ctx + tok0 + row / G;
         max_kv = min(qpos, e.seq - 1);
         min_kv = W > 0 ? max(0, qpos - W + 1) : 0;
@@ -846,24 +882,26 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
       // test hook: the group's first wait runs out (nothing arrives at bar.never)
       if (u == 0 && p.a.test_expire_wait && !mbar_wait_warp_polls(&bar.never, 0, kTestExpiryPolls))
         ok = false;
-      for (int j = 0; j < nkt && ok; ++j) {
+      // key tile j of the unit, or this group's half of it (NK keys from `off` on)
+      auto key_tile = [&](auto nk, int j, int off) {
+        constexpr int NK = decltype(nk)::value;
         if (!mbar_wait_warp_or_abort(&bar.s_full[t], (uint32_t)(swaits++ & 1), &bar.abort)) {
           ok = false;
-          break;
+          return;
         }
         tcgen05_fence_after();
-        uint32_t sr[kKeys];
+        uint32_t sr[NK];
 #pragma unroll
-        for (int c0 = 0; c0 < kKeys; c0 += 32)
+        for (int c0 = 0; c0 < NK; c0 += 32)
           tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(sr + c0));
         tmem_wait_ld();
         float* sv = reinterpret_cast<float*>(sr);
         // mask (bounds only; tiles inside every row's range need none) and row
         // maximum of the raw scores (the scale is positive, so it commutes with max)
-        const int key_base = (kt0 + j) * kKeys;
-        if (key_base < tile_min_kv_max || key_base + kKeys - 1 > tile_max_kv_min) {
+        const int key_base = (kt0 + j) * kKeys + off;
+        if (key_base < tile_min_kv_max || key_base + NK - 1 > tile_max_kv_min) {
 #pragma unroll
-          for (int c = 0; c < kKeys; ++c) {
+          for (int c = 0; c < NK; ++c) {
             const int key = key_base + c;
             if (key < min_kv || key > max_kv) sv[c] = -INFINITY;
           }
@@ -872,7 +910,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx8[k] = fmax3(sv[k], sv[8 + 2 * k], sv[9 + 2 * k]);
 #pragma unroll
-        for (int c = 24; c < kKeys; c += 2) mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], sv[c], sv[c + 1]);
+        for (int c = 24; c < NK; c += 2) mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], sv[c], sv[c + 1]);
         const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                fmaxf(mx8[6], mx8[7])) * sl2;
         const bool need = mx > m_ref + kRescaleLog2;
@@ -885,7 +923,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
         for (int k = 0; k < 8; ++k) sum8[k] = 0.f;
 #pragma unroll
-        for (int c = 0; c < kKeys; c += 2) {
+        for (int c = 0; c < NK; c += 2) {
           float x0, x1;
           ffma2(x0, x1, sv[c], sv[c + 1], sl2, -m_ref);
           sv[c] = ex2_approx(x0);
@@ -897,7 +935,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         l = l * alpha + sum;
         // P row as bf16 pairs over the first 64 columns of S_t (lane = row)
 #pragma unroll
-        for (int c0 = 0; c0 < kKeys; c0 += 32) {
+        for (int c0 = 0; c0 < NK; c0 += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(sv[c0 + 2 * i], sv[c0 + 2 * i + 1]);
@@ -921,14 +959,14 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // that 0 * V cannot produce a NaN (row index = key index in the tile).
         // Each group does it before its own P is signalled (the other group may
         // write the same zeros at the same time), so before either PV reads V.
-        if (key_base + kKeys > seq) {
+        if (key_base - off + kKeys > seq) {
           const int iv = i_base - 2 * (nkt - j) + 1;  // V_j of this unit
           if (!mbar_wait_warp_or_abort(&bar.full[iv % kStages], (uint32_t)((iv / kStages) & 1),
                                        &bar.abort)) {
             ok = false;
-            break;
+            return;
           }
-          if (key_base + row >= seq) {
+          if (key_base - off + row >= seq) {
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
 #pragma unroll
@@ -942,6 +980,13 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         tcgen05_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[t]);
+      };
+      if (kShared && !both) {
+        if constexpr (kShared)
+          for (int j = 0; j < nkt && ok; ++j)
+            key_tile(std::integral_constant<int, kKeys / 2>{}, j, t * (kKeys / 2));
+      } else {
+        for (int j = 0; j < nkt && ok; ++j) key_tile(std::integral_constant<int, kKeys>{}, j, 0);
       }
       // ---- epilogue: O / l for the rows of this tile. The rows' output offsets are
       // computed while the last PV product runs (~600 cycles after the wait otherwise).
@@ -953,11 +998,10 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
         for (int s4 = 0; s4 < 4; ++s4) {
           const int r = (warp & 3) * 32 + 4 * (lane >> 2) + s4;  // tile row
-          const int tok = (e.qt0 + t) * TQ + (r >> lg);
+          const int tok = (e.qt0 + (kShared && !both ? 0 : t)) * TQ + (r >> lg);
           if constexpr (kShared) {  // offset in the partial rows, four fp32 pieces a line
-            const long long base = (long long)p.part_row[ud->r] + (ud->pair >> 16) * e.q_len;
-            orow[s4] = tok < e.q_len ? ((base + tok) * p.a.num_q_heads + e.g * G + (r & (G - 1))) * D + q4 * 8
-                                     : -1;
+            const long long pr = partial_row(p, ud->r, ud->pair >> 16, t, both, e.tok0, tok);
+            orow[s4] = tok < e.q_len ? (pr * p.a.num_q_heads + e.g * G + (r & (G - 1))) * D + q4 * 8 : -1;
           } else {
             orow[s4] = tok < e.q_len ? ((long long)(e.q_start + tok) * p.a.num_q_heads + e.g * G +
                                         (r & (G - 1))) * D + q4 * 16
@@ -997,10 +1041,10 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
                            w[8 * s4 + 4], w[8 * s4 + 5], w[8 * s4 + 6], w[8 * s4 + 7]);
             }
           }
-          const int tok = kTiles * (ud->pair & 0xffff) * TQ + t * TQ + row / G;
-          const int n = ud->q_len;
-          if (tok < n)
-            p.part_ml[((long long)p.part_row[ud->r] + (ud->pair >> 16) * n + tok) * p.a.num_q_heads +
+          const int tok0 = kTiles * (ud->pair & 0xffff) * TQ;
+          const int tok = tok0 + (both ? t : 0) * TQ + row / G;
+          if (tok < ud->q_len)
+            p.part_ml[partial_row(p, ud->r, ud->pair >> 16, t, both, tok0, tok) * p.a.num_q_heads +
                       ud->g * G + (row & (G - 1))] = make_float2(m_ref, l);
         } else {
         const float inv = l > 0.f ? 1.f / l : 0.f;

@@ -59,11 +59,15 @@ struct PrefillArgs {
 // The same tiles over a prefix that the requests of a group share: an entry is a group, its
 // "request" r any of the group's (they have the same leading pages), its query tokens the group's
 // packed decode rows, seq_len the prefix's length; every row attends all of it. The key tiles are
-// split into units of tiles_per_unit, whose results are partial rows for the merge: token i of
-// entry e in split s is row part_row[e] + s * q_len + i.
+// split into units of tiles_per_unit, whose results are partial rows for the merge. A last query
+// tile without a second one beside it (the tail) is taken by two groups of warps instead, each with
+// one half of every key tile and a partial row of its own. With B the tokens before the
+// tail and R those in it, token i of entry e in split s is row part_row[e] + s B + i (i < B), or
+// rows tail_row[e] + (2 s + {0, 1}) R + i - B.
 struct PrefixArgs : PrefillArgs {
   int tiles_per_unit;
   int part_row[kPrefillMaxEntries];
+  int tail_row[kPrefillMaxEntries];
   float* part_o;    // [row][Hq][D] unnormalised
   float2* part_ml;  // [row][Hq] (running maximum in log2 units, sum)
 };

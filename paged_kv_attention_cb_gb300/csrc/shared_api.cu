@@ -32,7 +32,7 @@ constexpr int kMaxPrefixUnits = 4 * 192;     // units beyond one per (pair of ti
 
 // (row, head) entries of partial results: the decode pieces, and the prefix's.
 size_t partial_entries(int64_t R, int64_t T, int64_t Hq) {
-  return (size_t)(Hq * (R + kMaxDecodeCtasShared + T)) + (size_t)256 * kMaxPrefixUnits;
+  return (size_t)(Hq * (R + kMaxDecodeCtasShared + 2 * T)) + (size_t)256 * kMaxPrefixUnits;
 }
 
 size_t shared_bytes(int64_t R, int64_t T, int64_t Hq, int64_t D) {
@@ -40,10 +40,10 @@ size_t shared_bytes(int64_t R, int64_t T, int64_t Hq, int64_t D) {
   return cb::kWorkspaceHeaderBytes + align256(n * 8) + n * D * 4;
 }
 
-// Measured on GB300 (prefix of 8192, 64 and 148 rows of 4 and 8 heads): microseconds of one SM for
-// a 128-key tile against two query tiles and against one, and for a unit's start and its partial
-// rows. The decode stream as in plan.cu.
-constexpr double kPairUs = 1.5, kSingleUs = 1.0, kUnitUs = 3.5;
+// Measured on GB300 (32 and 16 rows of 8 heads, prefixes of 32768 and 131072): microseconds of one
+// SM for a 128-key tile against two query tiles and, in a tail, against one; and for a unit's
+// start and its partial rows. The decode stream as in plan.cu.
+constexpr double kPairUs = 2.05, kTailUs = 1.1, kUnitUs = 4.0;
 constexpr double kHbm = 6.6e12, kHbmPerSm = 75e9;
 
 // Below this many bytes of repeated prefix reads a plain step is faster: its decode kernel finds
@@ -65,26 +65,19 @@ struct SharedPlan {
 
 int rows_per_tile(const cb::StepArgs& a) { return 128 / (a.num_q_heads / a.num_kv_heads); }
 
-// SM-microseconds of the prefix tiles, without the units' own cost.
-double prefix_us(const SharedPlan& sp, const cb::StepArgs& a) {
-  double us = 0.0;
-  for (const Group& g : sp.groups) {
-    const int tiles = (g.rows + rows_per_tile(a) - 1) / rows_per_tile(a);
-    us += (double)cb::prefix_key_tiles(g.prefix) * a.num_kv_heads *
-          ((tiles / 2) * kPairUs + (tiles % 2) * kSingleUs);
-  }
-  return us;
+// A group's query tiles: pairs of them, a tail or none, and the tokens before the tail.
+struct Tiles {
+  int pairs, tail, body;
+};
+
+Tiles tiles_of(const Group& g, const cb::StepArgs& a) {
+  const int tq = rows_per_tile(a), tiles = (g.rows + tq - 1) / tq;
+  return Tiles{tiles / 2, tiles % 2, tiles % 2 ? (tiles - 1) * tq : g.rows};
 }
 
-// Units and partial rows for a split of the key tiles into units of `per`.
-void count_units(const SharedPlan& sp, const cb::StepArgs& a, int per, long long* units, long long* rows) {
-  *units = *rows = 0;
-  for (const Group& g : sp.groups) {
-    const int tiles = (g.rows + rows_per_tile(a) - 1) / rows_per_tile(a);
-    const int splits = cb::prefix_splits(g.prefix, per);
-    *units += (long long)((tiles + 1) / 2) * a.num_kv_heads * splits;
-    *rows += (long long)g.rows * splits;
-  }
+int64_t partial_rows(const Group& g, const cb::StepArgs& a, int per) {
+  const Tiles t = tiles_of(g, a);
+  return (int64_t)cb::prefix_splits(g.prefix, per) * (t.body + 2 * (g.rows - t.body));
 }
 
 void plan_prefix(SharedPlan& sp, const cb::StepArgs& a, int per, int grid_max, int first_row) {
@@ -102,15 +95,76 @@ void plan_prefix(SharedPlan& sp, const cb::StepArgs& a, int per, int grid_max, i
   p.tiles_per_unit = per;
   int row = first_row;
   for (const Group& g : sp.groups) {
-    const int e = p.n_entries++;
-    p.entries[e] = cb::PrefillEntry{g.r, (g.rows + p.tile_tokens - 1) / p.tile_tokens, g.q_start, g.rows, g.prefix};
+    const Tiles t = tiles_of(g, a);
+    const int e = p.n_entries++, splits = cb::prefix_splits(g.prefix, per);
+    p.entries[e] = cb::PrefillEntry{g.r, 2 * t.pairs + t.tail, g.q_start, g.rows, g.prefix};
     p.part_row[e] = row;
-    const int splits = cb::prefix_splits(g.prefix, per);
-    p.total_units += (p.entries[e].n_qtiles + 1) / 2 * a.num_kv_heads * splits;
-    row += g.rows * splits;
+    p.tail_row[e] = row + splits * t.body;
+    p.total_units += (t.pairs + t.tail) * a.num_kv_heads * splits;
+    row += (int)partial_rows(g, a, per);
   }
   p.total_ctas = p.total_units;
   p.grid = std::min(p.total_units, grid_max);
+}
+
+// About when `units` pieces of work of `us` each are done by k SMs from the start and `rest` more
+// from `from` on.
+double done_at(long long units, double us, int k, int rest, double from) {
+  const long long before = k * (long long)(from / us);
+  if (units <= before) return us * (double)((units + k - 1) / k);
+  return from + us * (double)((units - before + k + rest - 1) / (k + rest));
+}
+
+struct Choice {
+  int k;    // SMs the decode grid leaves to the prefix grid
+  int per;  // key tiles per unit
+};
+
+// The SM share and the split of the key tiles with the least modelled time: the decode stream on
+// its SMs, the prefix's units on the others and then on all, and the merge of the partial rows
+// (written and read once at L2's rate).
+Choice choose(const SharedPlan& sp, const cb::StepArgs& a, double decode_bytes, int S, bool beside,
+              size_t max_rows) {
+  int longest = 0;
+  double tile_us = 0.0;  // of all key tiles
+  long long tile_units = 0;
+  for (const Group& g : sp.groups) {
+    const Tiles t = tiles_of(g, a);
+    const int n = cb::prefix_key_tiles(g.prefix);
+    tile_us += (double)n * a.num_kv_heads * (t.pairs * kPairUs + t.tail * kTailUs);
+    tile_units += (long long)n * a.num_kv_heads * (t.pairs + t.tail);
+    longest = std::max(longest, n);
+  }
+  const double mean_us = tile_us / (double)tile_units;
+  const double row_us = (double)a.num_q_heads * a.head_dim * 8 / 4e6;  // a partial row, both ways, on all SMs
+  Choice best{1, longest};
+  double best_t = 1e30;
+  // 1, 2, 3, 4, 6, 8, 12, 16, ...: finer steps would change the modelled time by less than its error
+  for (int p2 = 1, third = 0;; third ^= 1, p2 *= third ? 1 : 2) {
+    const int per = std::min(third ? p2 + p2 / 2 : p2, longest);
+    long long units = 0, rows = 0;
+    for (const Group& g : sp.groups) {
+      const Tiles t = tiles_of(g, a);
+      units += (long long)(t.pairs + t.tail) * a.num_kv_heads * cb::prefix_splits(g.prefix, per);
+      rows += partial_rows(g, a, per);
+    }
+    if ((size_t)rows <= max_rows || per == longest) {
+      const double us = per * mean_us + kUnitUs;
+      for (int k = 4; k < S; k += 6) {
+        const double td = beside ? decode_bytes / std::min(kHbm, (S - k) * kHbmPerSm) * 1e6
+                                 : decode_bytes / kHbm * 1e6;
+        const double tp = beside ? done_at(units, us, k, S - k, td) : td + done_at(units, us, S, 0, 0.0);
+        const double t = std::max(td, tp) + (double)rows * row_us;
+        if (t < best_t * (1 - 1e-9)) {
+          best_t = t;
+          best = Choice{k, per};
+        }
+        if (!beside) break;
+      }
+    }
+    if (per == longest) break;
+  }
+  return best;
 }
 
 // False: the step is better run plainly, or needs a kernel the shared form does not cover.
@@ -152,43 +206,17 @@ bool plan_shared(SharedPlan& sp, const cb::StepArgs& a, const int32_t* qsl, cons
     if (qsl[r + 1] - qsl[r] == 1) U += cb::decode_units_host(seq[r], 0, prefix[r]);
   const int S = std::min(cb::sm_count(), kMaxDecodeCtasShared);
   const int hg = a.num_kv_heads / plan.decode.heads_per_cta;
-  // ---- SMs for the prefix: least modelled time of the decode on S - k SMs and the prefix on k,
-  // then on all
-  const double tiles_us = prefix_us(sp, a);
-  int k = 0;
-  if (plan.concurrent) {
-    const double bytes = (double)U * 16 * 2 * a.num_kv_heads * a.head_dim * 2;
-    double best = 1e30;
-    for (int c = 1; c < S; ++c) {
-      const double td = bytes / std::min(kHbm, (S - c) * kHbmPerSm) * 1e6;
-      const double left = tiles_us + c * kUnitUs - c * td;
-      const double t = left > 0 ? td + left / S : std::max(td, tiles_us / c + kUnitUs);
-      if (t < best * (1 - 1e-9)) {
-        best = t;
-        k = c;
-      }
-    }
-  }
-  // ---- units: as many as the SMs that work on the prefix, whole key tiles, no more partial rows
-  // than the workspace holds
-  long long tile_pairs = 0;
-  for (const Group& g : sp.groups)
-    tile_pairs += (long long)cb::prefix_key_tiles(g.prefix) * a.num_kv_heads *
-                  ((g.rows + 2 * rows_per_tile(a) - 1) / (2 * rows_per_tile(a)));
-  // (a decode grid larger than its SMs would hold the prefix grid back until its last CTAs start)
-  const int C = std::max(1, (plan.concurrent ? S - k : S) / hg);
-  const double td_us = (double)U * 16 * 2 * a.num_kv_heads * a.head_dim * 2 / std::min(kHbm, C * hg * kHbmPerSm) * 1e6;
-  const bool behind = plan.concurrent && tiles_us <= k * td_us;  // done while the decode streams
-  const long long target = behind ? k : 2 * S;
-  int per = (int)std::max<long long>(1, (tile_pairs + target - 1) / target);
-  const long long slots = a.num_requests + C;
   const size_t entries = partial_entries(a.num_requests, a.num_tokens, a.num_q_heads);
-  long long units = 0, rows = 0;
-  for (;; per *= 2) {
-    count_units(sp, a, per, &units, &rows);
-    if ((size_t)(slots + rows) * a.num_q_heads <= entries) break;
-    if (per > 1 << 24) return false;
-  }
+  const size_t slots_max = (size_t)a.num_requests + S;
+  const double bytes = (double)U * 16 * 2 * a.num_kv_heads * a.head_dim * 2;
+  const Choice ch = choose(sp, a, bytes, S, plan.concurrent, entries / a.num_q_heads - slots_max);
+  const int per = ch.per;
+  // (a decode grid larger than its SMs would hold the prefix grid back until its last CTAs start)
+  const int C = std::max(1, (plan.concurrent ? S - ch.k : S) / hg);
+  const long long slots = a.num_requests + C;
+  size_t rows = 0;
+  for (const Group& g : sp.groups) rows += (size_t)partial_rows(g, a, per);
+  if ((slots + rows) * a.num_q_heads > entries) return false;
   cb::plan_decode(plan, a, qsl, seq, prefix, U, C, scatter);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   plan.decode.part_ml = reinterpret_cast<float2*>(ws + cb::kWorkspaceHeaderBytes);
@@ -209,9 +237,11 @@ bool plan_shared(SharedPlan& sp, const cb::StepArgs& a, const int32_t* qsl, cons
     cb::MergeRow m{qsl[r], r + b0, 1, b1 - b0 + 1, 0, 0, 0};
     if (sp.group_of[r] >= 0) {
       const Group& g = sp.groups[sp.group_of[r]];
-      m.b = sp.prefix.part_row[sp.group_of[r]] + (qsl[r] - g.q_start);
-      m.b_step = g.rows;
-      m.nb = cb::prefix_splits(g.prefix, per);
+      const int e = sp.group_of[r], i = qsl[r] - g.q_start, body = tiles_of(g, a).body;
+      const bool tail = i >= body;
+      m.b = tail ? sp.prefix.tail_row[e] + i - body : sp.prefix.part_row[e] + i;
+      m.b_step = tail ? g.rows - body : body;
+      m.nb = cb::prefix_splits(g.prefix, per) * (tail ? 2 : 1);
     } else if (b1 == b0) {
       continue;
     }
