@@ -41,14 +41,16 @@ size_t shared_bytes(int64_t R, int64_t T, int64_t Hq, int64_t D) {
 }
 
 // Measured on GB300 (32 and 16 rows of 8 heads, prefixes of 32768 and 131072): microseconds of one
-// SM for a 128-key tile against two query tiles and, in a tail, against one; and for a unit's
-// start and its partial rows. The decode stream as in plan.cu.
-constexpr double kPairUs = 2.05, kTailUs = 1.1, kUnitUs = 4.0;
-constexpr double kHbm = 6.6e12, kHbmPerSm = 75e9;
+// SM for a 128-key tile against two query tiles (tensor pipe and softmax) and, in a tail, against
+// one (the keys' bytes: 5.3 TB/s over all SMs); and for a unit's start and its partial rows.
+constexpr double kPairUs = 2.05, kTailUs = 1.85, kUnitUs = 4.0;
+constexpr double kHbm = 6.6e12;
 
-// Below this many bytes of repeated prefix reads a plain step is faster: its decode kernel finds
-// the shared pages in L2 after the first request's read.
-constexpr double kWorthBytes = 24e6;
+// The plain step, which reads the shared pages from L2 after the first request: a start of 9 us
+// and 0.82 us a key block of its decode partition (64 requests behind 8192 positions, 32/8 heads:
+// 187 us; 16 behind 512: 12.6 us). The shared form's launches and merge on top of its model: 9.5 us
+// (16 requests behind 2048 positions: 14.7 us shared, 20.7 plain; behind 512: 14.2 and 12.6).
+constexpr double kPlainUs = 9.0, kPlainBlockUs = 0.82, kSharedUs = 9.5;
 
 struct Group {
   int r, q_start, rows, prefix;
@@ -107,24 +109,35 @@ void plan_prefix(SharedPlan& sp, const cb::StepArgs& a, int per, int grid_max, i
   p.grid = std::min(p.total_units, grid_max);
 }
 
-// About when `units` pieces of work of `us` each are done by k SMs from the start and `rest` more
-// from `from` on.
+// When `units` pieces of work of `us` each are done by k SMs from the start and `rest` more from
+// `from` on.
 double done_at(long long units, double us, int k, int rest, double from) {
-  const long long before = k * (long long)(from / us);
-  if (units <= before) return us * (double)((units + k - 1) / k);
-  return from + us * (double)((units - before + k + rest - 1) / (k + rest));
+  auto done = [&](double t) {
+    return k * (long long)(t / us) + (t > from ? rest * (long long)((t - from) / us) : 0);
+  };
+  constexpr double kEps = 1e-6;
+  double t = ((double)units * us + (rest > 0 ? rest * from : 0.0)) / (k + rest);  // no sooner
+  if (t < from) t = (double)units * us / k;
+  for (int i = 0; i < 8 && done(t + kEps) < units; ++i) {
+    // the next time at which an SM of either kind finishes a piece
+    const double a = (floor(t / us + kEps) + 1) * us;
+    const double b = t < from ? from + us : from + (floor((t - from) / us + kEps) + 1) * us;
+    t = rest > 0 ? std::min(a, b) : a;
+  }
+  return t;
 }
 
 struct Choice {
-  int k;    // SMs the decode grid leaves to the prefix grid
-  int per;  // key tiles per unit
+  int k;      // SMs the decode grid leaves to the prefix grid
+  int per;    // key tiles per unit
+  double us;  // modelled time
 };
 
 // The SM share and the split of the key tiles with the least modelled time: the decode stream on
 // its SMs, the prefix's units on the others and then on all, and the merge of the partial rows
 // (written and read once at L2's rate).
-Choice choose(const SharedPlan& sp, const cb::StepArgs& a, double decode_bytes, int S, bool beside,
-              size_t max_rows) {
+Choice choose(const SharedPlan& sp, const cb::StepArgs& a, double decode_bytes, double decode_blocks,
+              int S, bool beside, size_t max_rows) {
   int longest = 0;
   double tile_us = 0.0;  // of all key tiles
   long long tile_units = 0;
@@ -137,32 +150,38 @@ Choice choose(const SharedPlan& sp, const cb::StepArgs& a, double decode_bytes, 
   }
   const double mean_us = tile_us / (double)tile_units;
   const double row_us = (double)a.num_q_heads * a.head_dim * 8 / 4e6;  // a partial row, both ways, on all SMs
-  Choice best{1, longest};
-  double best_t = 1e30;
-  // 1, 2, 3, 4, 6, 8, 12, 16, ...: finer steps would change the modelled time by less than its error
-  for (int p2 = 1, third = 0;; third ^= 1, p2 *= third ? 1 : 2) {
-    const int per = std::min(third ? p2 + p2 / 2 : p2, longest);
+  Choice best{4, longest, 1e30};
+  // key tiles a unit: 1, 2, 3, 4, 6, 8, 12, 16, ..., and what makes 1 to 4 units per SM
+  int candidates[80], n_candidates = 0;
+  for (int waves = 1; waves <= 4; ++waves)
+    candidates[n_candidates++] = (int)((tile_units + (long long)waves * S - 1) / ((long long)waves * S));
+  for (int p2 = 1; p2 < longest; p2 *= 2) {
+    candidates[n_candidates++] = p2;
+    candidates[n_candidates++] = p2 + p2 / 2;
+  }
+  candidates[n_candidates++] = longest;
+  for (int c = 0; c < n_candidates; ++c) {
+    const int per = std::min(candidates[c], longest);
+    if (std::find(candidates, candidates + c, per) != candidates + c) continue;
     long long units = 0, rows = 0;
     for (const Group& g : sp.groups) {
       const Tiles t = tiles_of(g, a);
       units += (long long)(t.pairs + t.tail) * a.num_kv_heads * cb::prefix_splits(g.prefix, per);
       rows += partial_rows(g, a, per);
     }
-    if ((size_t)rows <= max_rows || per == longest) {
+    if ((size_t)rows <= max_rows) {
       const double us = per * mean_us + kUnitUs;
-      for (int k = 4; k < S; k += 6) {
-        const double td = beside ? decode_bytes / std::min(kHbm, (S - k) * kHbmPerSm) * 1e6
-                                 : decode_bytes / kHbm * 1e6;
+      for (int k = 4; k < S; k += k < 28 ? 8 : 14) {
+        const double td = std::max(decode_bytes / kHbm * 1e6,
+                                   decode_blocks * kPlainBlockUs / (beside ? S - k : S));
+        const double merge = (double)rows * row_us;
+        if (std::max(td, (double)units * us / S) + merge >= best.us * 0.97) continue;  // cannot be better
         const double tp = beside ? done_at(units, us, k, S - k, td) : td + done_at(units, us, S, 0, 0.0);
-        const double t = std::max(td, tp) + (double)rows * row_us;
-        if (t < best_t * (1 - 1e-9)) {
-          best_t = t;
-          best = Choice{k, per};
-        }
+        const double t = std::max(td, tp) + merge;
+        if (t < best.us * 0.97) best = Choice{k, per, t};  // (few SMs for the prefix where it makes no odds)
         if (!beside) break;
       }
     }
-    if (per == longest) break;
   }
   return best;
 }
@@ -176,7 +195,6 @@ bool plan_shared(SharedPlan& sp, const cb::StepArgs& a, const int32_t* qsl, cons
   sp.merge.clear();
   sp.group_of.assign(a.num_requests, -1);
   sp.max_pieces = 0;
-  double saved = 0.0;
   for (int g = 0; g < n_groups; ++g) {
     Group gr{-1, 0, 0, 0};
     for (int r = group_start[g]; r < group_start[g + 1]; ++r) {
@@ -186,11 +204,9 @@ bool plan_shared(SharedPlan& sp, const cb::StepArgs& a, const int32_t* qsl, cons
       sp.group_of[r] = (int)sp.groups.size();
     }
     if (gr.rows == 0) continue;
-    saved += (double)(gr.rows - 1) * gr.prefix * a.num_kv_heads * a.head_dim * 4;
     sp.groups.push_back(gr);
   }
   if (sp.groups.empty() || sp.groups.size() > cb::kPrefillMaxEntries) return false;
-  if (saved < kWorthBytes && !(flags & CB_FLAG_SHARE_ALWAYS)) return false;
 
   cb::Plan& plan = sp.plan;
   cb::plan_step(plan, a, qsl, seq, flags, nullptr, workspace, workspace_bytes);
@@ -201,16 +217,21 @@ bool plan_shared(SharedPlan& sp, const cb::StepArgs& a, const int32_t* qsl, cons
   plan.concurrent = plan.n_prefill_launches == 0;
   plan.fused_scatter = scatter != nullptr && plan.concurrent;
 
-  long long U = 0;
-  for (int r = 0; r < a.num_requests; ++r)
-    if (qsl[r + 1] - qsl[r] == 1) U += cb::decode_units_host(seq[r], 0, prefix[r]);
+  long long U = 0, U_plain = 0;
+  for (int r = 0; r < a.num_requests; ++r) {
+    if (qsl[r + 1] - qsl[r] != 1) continue;
+    U += cb::decode_units_host(seq[r], 0, prefix[r]);
+    U_plain += cb::decode_units_host(seq[r], 0, 0);
+  }
   const int S = std::min(cb::sm_count(), kMaxDecodeCtasShared);
   const int hg = a.num_kv_heads / plan.decode.heads_per_cta;
   const size_t entries = partial_entries(a.num_requests, a.num_tokens, a.num_q_heads);
   const size_t slots_max = (size_t)a.num_requests + S;
   const double bytes = (double)U * 16 * 2 * a.num_kv_heads * a.head_dim * 2;
-  const Choice ch = choose(sp, a, bytes, S, plan.concurrent, entries / a.num_q_heads - slots_max);
+  const Choice ch = choose(sp, a, bytes, (double)U * hg, S, plan.concurrent, entries / a.num_q_heads - slots_max);
   const int per = ch.per;
+  const double plain_us = kPlainUs + kPlainBlockUs * (double)U_plain * hg / S;
+  if (ch.us + kSharedUs >= plain_us && !(flags & CB_FLAG_SHARE_ALWAYS)) return false;
   // (a decode grid larger than its SMs would hold the prefix grid back until its last CTAs start)
   const int C = std::max(1, (plan.concurrent ? S - ch.k : S) / hg);
   const long long slots = a.num_requests + C;
