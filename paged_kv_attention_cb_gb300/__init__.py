@@ -12,7 +12,7 @@ import os
 
 import numpy as np
 
-from .build import LIB_PATH
+from .build import BINDING_PATH, LIB_PATH
 
 CB_F32 = 0
 CB_BF16 = 1
@@ -347,151 +347,32 @@ def no_alloc_read_error_word(stream=None) -> int:
 
 # ------------------------------------------------- checked calls (8-bit cache, shared prefixes)
 #
-# These entry points check every tensor (type, shape, contiguity, device) before the call. The
-# checks run on whole lists at once: a small decode step takes ~10 us on the GPU, and a Python
-# statement per tensor and property took longer than that.
+# These entry points check every tensor's type, shape, contiguity and device before the call, in a
+# native module (csrc/torch_binding.cpp): as Python statements the checks took longer than a small
+# decode step does on the GPU.
+
+_BINDING = None
 
 
-class _Torch:
-    """torch's types and methods that the checks use, looked up on first use (the module itself
-    imports without torch)."""
+def _binding():
+    """The native module of checked calls, bound to the loaded libcb (raises if not built)."""
+    global _BINDING
+    if _BINDING is None:
+        import importlib.util
 
-    def __init__(self):
-        import torch
+        import torch  # noqa: F401  (the module works on its tensors)
 
-        self.e4m3 = (torch.float8_e4m3fn, torch.uint8)
-        self.e8m0 = (torch.float8_e8m0fnu, torch.uint8)
-        self.i32, self.i64 = torch.int32, torch.int64
-        self.code = {torch.float32: CB_F32, torch.bfloat16: CB_BF16}
-        self.device_of = torch.Tensor.get_device
-        self.contiguous = torch.Tensor.is_contiguous
-        self.ptr = torch.Tensor.data_ptr
-        self.current_device = torch.cuda.current_device
-        self.device = torch.cuda.device
-        # the raw handle of the current stream; the public call wraps it in an object first
-        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda d: torch.cuda.current_stream(d).cuda_stream)
-
-
-_TORCH = None
-_NP_I32 = np.dtype(np.int32)
-_addressof, _from_buffer = ctypes.addressof, ctypes.c_char.from_buffer
-
-
-def _torch() -> _Torch:
-    global _TORCH
-    if _TORCH is None:
-        _TORCH = _Torch()
-    return _TORCH
-
-
-def _pointers(tensors, shapes, dtypes, names):
-    """The data pointers of contiguous tensors of these shapes and dtypes, all on one CUDA device,
-    and its index. ``names``: a function that gives their names, for the error."""
-    t = _torch()
-    device = t.device_of(tensors[0])
-    if (device >= 0 and tuple([x.shape for x in tensors]) == shapes
-            and tuple([x.dtype for x in tensors]) == dtypes and all(map(t.contiguous, tensors))
-            and set(map(t.device_of, tensors)) == {device}):
-        return list(map(t.ptr, tensors)), device
-    names = names()
-    for x, name, shape, dtype in zip(tensors, names, shapes, dtypes):
-        if x.dtype != dtype:
-            raise CbError(1, f"{name}: dtype {x.dtype}, not {dtype}")
-        if tuple(x.shape) != tuple(shape):
-            raise CbError(1, f"{name}: shape {tuple(x.shape)}, not {tuple(shape)}")
-        if not x.is_contiguous():
-            raise CbError(1, f"{name} must be contiguous")
-        if not x.is_cuda or x.device != tensors[0].device:
-            raise CbError(1, f"{name} must be on the CUDA device of {names[0]}")
-    raise CbError(1, "tensors must be on a CUDA device")
-
-
-def _call(fn, device, stream, *args):
-    """fn(*args, stream) with the tensors' device current: the library launches on it."""
-    t = _torch()
-    if stream is None:
-        stream = t.stream(device)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    if device == t.current_device():
-        status = fn(*args, stream)
-    else:
-        with t.device(device):
-            status = fn(*args, stream)
-    if status:
-        _check(status)
-
-
-def _mirror(a, n, name):
-    """A host mirror as a contiguous int32 array of n entries, and its address (ndarray.ctypes takes
-    a microsecond; the buffer protocol a third of it, for writable arrays)."""
-    if type(a) is not np.ndarray or a.dtype != _NP_I32 or not a.flags.c_contiguous:
-        a = _host_i32(a)
-    if a.shape != (n,):
-        raise CbError(2, f"{name}: {a.shape} entries, not {n}")
-    if a.flags.writeable and n:
-        return a, _addressof(_from_buffer(a))
-    return a, a.ctypes.data
-
-
-def _dims(t, n, name):
-    if t.dim() != n:
-        raise CbError(1, f"{name}: {t.dim()} dimensions, not {n}")
-    return t.shape
-
-
-def _float_type(t, name):
-    code = _torch().code.get(t.dtype)
-    if code is None:
-        raise CbError(1, f"{name}: dtype {t.dtype}, not torch.float32 or torch.bfloat16")
-    return code
-
-
-# ---------------------------------------------------------------- 8-bit paged cache
-
-
-_CACHE_NAMES = ("k_cache", "v_cache", "k_scale", "v_scale")
-
-
-def _cache_q8(k_cache, v_cache, k_scale, v_scale):
-    """(tensors, shapes, dtypes) of an 8-bit cache."""
-    t = _torch()
-    shape = _dims(k_cache, 4, "k_cache")
-    value, scale = k_cache.dtype, k_scale.dtype
-    if value not in t.e4m3:
-        raise CbError(1, f"k_cache: dtype {value}, not {' or '.join(map(str, t.e4m3))}")
-    if scale not in t.e8m0:
-        raise CbError(1, f"k_scale: dtype {scale}, not {' or '.join(map(str, t.e8m0))}")
-    rows = shape[:3]
-    return ((k_cache, v_cache, k_scale, v_scale), (shape, shape, rows, rows),
-            (value, value, scale, scale))
-
-
-def _rows_q8(fn, rows, names, cache, slot_mapping, error_word, stream):
-    t = _torch()
-    a, b = rows
-    code = _float_type(a, names[0])
-    shape = T, Hkv, D = _dims(a, 3, names[0])
-    tensors, shapes, dtypes = _cache_q8(*cache)
-    NB, BS, H, Dc = shapes[0]
-    if H != Hkv or Dc != D:
-        raise CbError(1, f"k_cache: rows of {(H, Dc)}, not {(Hkv, D)}")
-    kind = a.dtype
-    tensors = (a, b, *tensors, slot_mapping)
-    shapes = (shape, shape, *shapes, (T,))
-    dtypes = (kind, kind, *dtypes, t.i64)
-    if error_word is not None:
-        tensors, shapes, dtypes = (*tensors, error_word), (*shapes, error_word.shape), (*dtypes, t.i32)
-    p, device = _pointers(tensors, shapes, dtypes,
-                          lambda: (*names, *_CACHE_NAMES, "slot_mapping", "error_word"))
-    word = p[7] if error_word is not None else None
-    if names[0] == "k_out":
-        _call(fn, device, stream, p[2], p[3], p[4], p[5], p[6], p[0], p[1], T, NB, BS, Hkv, D,
-              code, word)
-    else:
-        _call(fn, device, stream, p[0], p[1], p[2], p[3], p[4], p[5], p[6], T, NB, BS, Hkv, D,
-              code, word)
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"_cb_torch.so not built at {BINDING_PATH}: run "
+                               "paged_kv_attention_cb_gb300.build")
+        spec = importlib.util.spec_from_file_location("_cb_torch", BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(*[ctypes.cast(getattr(lib(), f), ctypes.c_void_p).value for f in (
+            "cb_write_kv_q8", "cb_read_kv_q8", "cb_paged_attention_q8",
+            "cb_paged_attention_shared", "cb_last_error_message")], CbError, _host_i32)
+        _BINDING = module
+    return _BINDING
 
 
 def write_kv_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping, error_word=None,
@@ -499,16 +380,16 @@ def write_kv_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, slot_mapping, 
     """Quantise k_new/v_new [T, Hkv, D] (bf16 or fp32) into the 8-bit caches [NB, BS, Hkv, D]
     (float8_e4m3fn) and their scales [NB, BS, Hkv] (float8_e8m0fnu) at slot_mapping [T].
     uint8 tensors are taken for either as well (see cb_write_kv_q8 in include/cb.h)."""
-    _rows_q8(lib().cb_write_kv_q8, (k_new, v_new), ("k_new", "v_new"),
-             (k_cache, v_cache, k_scale, v_scale), slot_mapping, error_word, stream)
+    (_BINDING or _binding()).write_kv_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale,
+                                         slot_mapping, error_word, stream)
 
 
 def read_kv_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping, k_out, v_out, error_word=None,
                stream=None):
     """k_out/v_out [T, Hkv, D] (bf16 or fp32) = the 8-bit caches' rows at slot_mapping [T]
     (rows of negative slots stay as they are; see cb_read_kv_q8 in include/cb.h)."""
-    _rows_q8(lib().cb_read_kv_q8, (k_out, v_out), ("k_out", "v_out"),
-             (k_cache, v_cache, k_scale, v_scale), slot_mapping, error_word, stream)
+    (_BINDING or _binding()).read_kv_q8(k_out, v_out, k_cache, v_cache, k_scale, v_scale,
+                                        slot_mapping, error_word, stream)
 
 
 def workspace_size_q8(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim, block_size,
@@ -527,45 +408,6 @@ def alloc_workspace_q8(num_requests, num_tokens, num_q_heads, num_kv_heads, head
     return torch.zeros((n + 15) // 16 * 16, dtype=torch.uint8, device=device)
 
 
-_STEP_NAMES = ("q", "out", "query_start_loc", "seq_lens", "block_table", "workspace")
-_NEW_NAMES = ("k_new", "v_new", "slot_mapping")
-
-
-def _step(out, q, query_start_loc, seq_lens, block_table, workspace, cache, cache_names, k_new,
-          v_new, slot_mapping):
-    """Checks the tensors of a step over `cache` (tensors, shapes, dtypes; the first one the K
-    cache). Returns the pointers -- q, out, query_start_loc, seq_lens, block_table, workspace,
-    cache..., k_new, v_new, slot_mapping -- the device, and the sizes."""
-    t = _torch()
-    code = _float_type(q, "q")
-    qs = T, Hq, D = _dims(q, 3, "q")
-    (R,) = rs = _dims(seq_lens, 1, "seq_lens")
-    stride = _dims(block_table, 2, "block_table")[1]
-    ctensors, cshapes, cdtypes = cache
-    NB, BS, Hkv, Dc = cshapes[0]
-    if Dc != D:
-        raise CbError(1, f"k_cache: head_dim {Dc}, not {D}")
-    i32, kind = t.i32, q.dtype
-    if k_new is not None:
-        if v_new is None or slot_mapping is None:
-            raise CbError(1, "k_new given without v_new or slot_mapping")
-        rows = (T, Hkv, D)
-        p, device = _pointers(
-            (q, out, query_start_loc, seq_lens, block_table, workspace, *ctensors, k_new, v_new,
-             slot_mapping),
-            (qs, qs, (R + 1,), rs, (R, stride), workspace.shape, *cshapes, rows, rows, (T,)),
-            (kind, kind, i32, i32, i32, workspace.dtype, *cdtypes, kind, kind, t.i64),
-            lambda: (*_STEP_NAMES, *cache_names, *_NEW_NAMES))
-    else:
-        p, device = _pointers(
-            (q, out, query_start_loc, seq_lens, block_table, workspace, *ctensors),
-            (qs, qs, (R + 1,), rs, (R, stride), workspace.shape, *cshapes),
-            (kind, kind, i32, i32, i32, workspace.dtype, *cdtypes),
-            lambda: (*_STEP_NAMES, *cache_names))
-        p += (None, None, None)
-    return p, device, code, T, Hq, D, R, stride, NB, BS, Hkv
-
-
 def paged_attention_q8(out, q, k_cache, v_cache, k_scale, v_scale, query_start_loc, seq_lens,
                        block_table, h_query_start_loc, h_seq_lens, workspace, *, scale=0.0,
                        sliding_window=0, k_new=None, v_new=None, slot_mapping=None, flags=0,
@@ -576,19 +418,11 @@ def paged_attention_q8(out, q, k_cache, v_cache, k_scale, v_scale, query_start_l
     [NB, BS, Hkv] float8_e8m0fnu (or uint8); the step's k_new/v_new are quantised into their
     slots first. workspace: alloc_workspace_q8.
     """
-    p, device, dtype, T, Hq, D, R, stride, NB, BS, Hkv = _step(
-        out, q, query_start_loc, seq_lens, block_table, workspace,
-        _cache_q8(k_cache, v_cache, k_scale, v_scale), _CACHE_NAMES, k_new, v_new, slot_mapping)
-    hq, hq_at = _mirror(h_query_start_loc, R + 1, "h_query_start_loc")
-    hs, hs_at = _mirror(h_seq_lens, R, "h_seq_lens")
-    pq, pout, pqsl, pseq, pbt, pws, pk, pv, pks, pvs, pkn, pvn, psl = p
-    _call(lib().cb_paged_attention_q8, device, stream, pout, pq, pk, pv, pks, pvs, pkn, pvn, psl,
-          pqsl, pseq, pbt, stride, hq_at, hs_at, R, T, NB, BS, Hq, Hkv, D, scale, sliding_window,
-          dtype, flags, pws, workspace.numel() * workspace.element_size())
+    (_BINDING or _binding()).paged_attention_q8(
+        out, q, k_cache, v_cache, k_scale, v_scale, query_start_loc, seq_lens, block_table,
+        h_query_start_loc, h_seq_lens, workspace, scale, sliding_window, k_new, v_new,
+        slot_mapping, flags, stream)
     return out
-
-
-# ---------------------------------------------------------------- shared prefixes
 
 
 def workspace_size_shared(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim) -> int:
@@ -616,23 +450,10 @@ def paged_attention_shared(out, q, k_cache, v_cache, query_start_loc, seq_lens, 
     shares with its group; h_group_start [n_groups + 1] on the host: group g is the requests
     h_group_start[g] .. h_group_start[g + 1] - 1. workspace: alloc_workspace_shared.
     """
-    shape = _dims(k_cache, 4, "k_cache")
-    cache = ((k_cache, v_cache, prefix_lens), (shape, shape, seq_lens.shape),
-             (q.dtype, q.dtype, _torch().i32))
-    p, device, dtype, T, Hq, D, R, stride, NB, BS, Hkv = _step(
-        out, q, query_start_loc, seq_lens, block_table, workspace, cache,
-        ("k_cache", "v_cache", "prefix_lens"), k_new, v_new, slot_mapping)
-    groups = len(h_group_start) - 1
-    if groups < 0:
-        raise CbError(2, "h_group_start must have n_groups + 1 entries")
-    hq, hq_at = _mirror(h_query_start_loc, R + 1, "h_query_start_loc")
-    hs, hs_at = _mirror(h_seq_lens, R, "h_seq_lens")
-    hp, hp_at = _mirror(h_prefix_lens, R, "h_prefix_lens")
-    hg, hg_at = _mirror(h_group_start, groups + 1, "h_group_start")
-    pq, pout, pqsl, pseq, pbt, pws, pk, pv, ppl, pkn, pvn, psl = p
-    _call(lib().cb_paged_attention_shared, device, stream, pout, pq, pk, pv, pkn, pvn, psl, pqsl,
-          pseq, pbt, stride, ppl, hq_at, hs_at, hp_at, hg_at, groups, R, T, NB, BS, Hq, Hkv, D,
-          scale, sliding_window, dtype, flags, pws, workspace.numel() * workspace.element_size())
+    (_BINDING or _binding()).paged_attention_shared(
+        out, q, k_cache, v_cache, query_start_loc, seq_lens, block_table, prefix_lens,
+        h_query_start_loc, h_seq_lens, h_prefix_lens, h_group_start, workspace, scale,
+        sliding_window, k_new, v_new, slot_mapping, flags, stream)
     return out
 
 

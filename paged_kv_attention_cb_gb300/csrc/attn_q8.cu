@@ -95,6 +95,12 @@ struct Q8Smem {
   int abort_flag;
 };
 
+// Bytes of a warp's query fragments. They stay in shared memory: in registers they made the key
+// loop spill (16 of 96 registers, twice that for fp32 queries).
+__host__ __device__ constexpr int q_frag_bytes(int D, int NB, bool f32) {
+  return D / 16 * NB * (f32 ? 2 : 1) * 256;
+}
+
 // Position of key row i (0 .. 15) of a tile within its block. For D 64 (64-byte rows) the low
 // two bits change places, so that the rows of a V fragment (2t, t = 0 .. 3) fall on both
 // halves of the banks.
@@ -174,6 +180,9 @@ CB_DEV int lds_u8(uint32_t addr) {
 CB_DEV void sts32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+CB_DEV void sts64(uint32_t addr, uint32_t x, uint32_t y) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(x), "r"(y) : "memory");
+}
 CB_DEV void sts8(uint32_t addr, int v) {
   asm volatile("st.shared.b8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -228,7 +237,8 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
   const int scale_bytes = kKB * Hkv;       // K (or V) scales of one block, every head
   uint8_t* stages = base;
   uint8_t* scales = stages + p.stages * stage_bytes;
-  Q8Smem& sm = *reinterpret_cast<Q8Smem*>(scales + p.stages * 2 * scale_bytes);
+  uint8_t* qfrags = scales + p.stages * 2 * scale_bytes;
+  Q8Smem& sm = *reinterpret_cast<Q8Smem*>(qfrags + HB * KW * CW * q_frag_bytes(D, NB, F32));
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -489,6 +499,8 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       const uint32_t v_off =
           box_bytes + (D == 128 ? row_chunk<D>(hl * kKB + key_of_row<D>(2 * tq), gid)
                                 : row_chunk<D>(hl * kKB + key_of_row<D>(2 * tq), gid >> 1) + (gid & 1) * 8);
+      // this warp's query fragments: a lane's 8 bytes of each step, column block and fp16 part
+      const uint32_t q_at = smem_u32(qfrags) + warp * q_frag_bytes(D, NB, F32) + lane * 8;
       int i0 = 0;                // block index of the piece's first block
       int s = kw, round = 0;     // stage and round of this warp's next block (kw, kw + KW, ...)
       for (int k = 0;; ++k) {
@@ -555,7 +567,6 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
         }
 
         // ---- q: column 8 nb + gid, d = D/4 tq .. + D/4 - 1, as fp16 fragments
-        uint32_t qf[NB][kKS][2 * kSplit];
         float cs0[NB], cs1[NB];  // score factors of columns 8 nb + 2 tq, + 1
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -591,14 +602,19 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
           cs1[nb] = __shfl_sync(0xffffffffu, cs, 8 * tq + 4);
 #pragma unroll
           for (int ks = 0; ks < kKS; ++ks) {
+            uint32_t w[2];
+            uint32_t rest[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float lo = value(4 * ks + 2 * e) * up, hi = value(4 * ks + 2 * e + 1) * up;
-              qf[nb][ks][e] = pack_f16x2(lo, hi);
-              if constexpr (F32) qf[nb][ks][2 + e] = pack_f16x2_rest(qf[nb][ks][e], lo, hi);
+              w[e] = pack_f16x2(lo, hi);
+              if constexpr (F32) rest[e] = pack_f16x2_rest(w[e], lo, hi);
             }
+            sts64(q_at + ((ks * NB + nb) * kSplit) * 256, w[0], w[1]);
+            if constexpr (F32) sts64(q_at + ((ks * NB + nb) * kSplit + 1) * 256, rest[0], rest[1]);
           }
         }
+        __syncwarp();
 
         float o[NB][kKS][4];
         float m[NB][2], mw[NB][2], l[NB][2];
@@ -673,9 +689,13 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
               const uint32_t a[4] = {f16x2_lo(wa[e]), f16x2_lo(wb[e]), f16x2_hi(wa[e]), f16x2_hi(wb[e])};
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb) {
-                const uint32_t(&q)[2 * kSplit] = qf[nb][4 * half + e];
-                mma_f16_16816(sc_[e & 1][nb], a, q[0], q[1]);
-                if constexpr (F32) mma_f16_16816(sc_[2][nb], a, q[2], q[3]);
+                const uint32_t at = q_at + (((4 * half + e) * NB + nb) * kSplit) * 256;
+                const uint2 q = lds64(at);
+                mma_f16_16816(sc_[e & 1][nb], a, q.x, q.y);
+                if constexpr (F32) {
+                  const uint2 rest = lds64(at + 256);
+                  mma_f16_16816(sc_[2][nb], a, rest.x, rest.y);
+                }
               }
             }
           }
@@ -1039,8 +1059,13 @@ cudaError_t cache_map(CUtensorMap* map, void* cache, const StepArgs& a, int hb) 
 template <int D, int NB, bool F32>
 cudaError_t launch_split_t(const Q8Args& p, cudaStream_t s) {
   auto kern = q8_split_kernel<D, NB, F32>;
-  const size_t smem = q8_smem_bytes(D, p.heads_per_cta, p.stages, p.a.num_kv_heads);
-  if (smem > (size_t)kQ8SmemLimit) return cudaErrorInvalidValue;
+  const size_t smem = q8_smem_bytes(D, p.heads_per_cta, p.heads_per_cta * p.key_warps * p.column_warps, NB, F32,
+                                    p.stages, p.a.num_kv_heads);
+  // a stage belongs to one producer and one key warp, which see every one of its phases
+  if (smem > (size_t)kQ8SmemLimit || p.stages < kQ8Producers || p.stages % kQ8Producers != 0 ||
+      p.stages % p.key_warps != 0 || p.stages > kQ8MaxStages ||
+      p.heads_per_cta * p.key_warps * p.column_warps > (NB == 1 ? 16 : 8))
+    return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8SmemLimit);
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
@@ -1080,9 +1105,9 @@ cudaError_t launch_portable_t(const StepArgs& a, const Q8Cache& c, cudaStream_t 
 
 }  // namespace
 
-size_t q8_smem_bytes(int D, int HB, int stages, int Hkv) {
+size_t q8_smem_bytes(int D, int HB, int warps, int NB, bool f32, int stages, int Hkv) {
   return 1024 /* alignment slack */ + (size_t)stages * (2 * HB * kKB * D + 2 * kKB * Hkv) +
-         sizeof(Q8Smem);
+         (size_t)warps * q_frag_bytes(D, NB, f32) + sizeof(Q8Smem);
 }
 
 cudaError_t launch_q8_split(const Q8Args& p, int column_blocks, cudaStream_t stream) {

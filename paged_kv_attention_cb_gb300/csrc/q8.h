@@ -41,7 +41,7 @@ constexpr int kQ8SmemLimit = 232448; // 227 KiB dynamic shared memory per CTA
 // only takes L1 away from the query rows and the few spilled registers (16 requests x 32768: 168
 // us with 132 KB of stages, 177 with 198 KB, 211 with 66 KB).
 constexpr int kQ8RingBytes = 136 * 1024;
-constexpr int kQ8MinBlocksPerCta = 4;
+constexpr int kQ8MinBlocksPerCta = 2;
 
 // Where a CTA's range of key blocks starts (the entry behind the last CTA: the end of all).
 struct Q8CtaStart {
@@ -78,7 +78,7 @@ struct Q8Args {
 
 // Column blocks (of 8 columns) per warp: 1 or 2.
 cudaError_t launch_q8_split(const Q8Args& p, int column_blocks, cudaStream_t stream);
-size_t q8_smem_bytes(int D, int HB, int stages, int Hkv);
+size_t q8_smem_bytes(int D, int HB, int warps, int NB, bool f32, int stages, int Hkv);
 
 // One warp per (row, KV head) on the CUDA cores: every shape, no split.
 cudaError_t launch_q8_portable(const StepArgs& a, const Q8Cache& c, cudaStream_t stream);

@@ -84,7 +84,7 @@ struct Item {
 // What starting and finishing a piece of an item costs a CTA, in key blocks: its query rows, the
 // first maximum, the partial rows (64 requests of 128 .. 2048 positions: CTAs with one piece were
 // done after 23.1 us, with two after 25.9, with three after 28.7; a block takes 0.8).
-constexpr int kPieceBlocks = 3;
+constexpr int kPieceBlocks = 4;
 
 struct Q8Plan {
   std::vector<Item> items;
@@ -126,8 +126,11 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
   const int HB = p.heads_per_cta = sp.heads;
   p.column_warps = sp.column_warps;
   p.key_warps = sp.key_warps;
-  const size_t fixed = cb::q8_smem_bytes(a.head_dim, HB, 0, a.num_kv_heads);
-  const size_t per = cb::q8_smem_bytes(a.head_dim, HB, 1, a.num_kv_heads) - fixed;
+  const int warps = HB * p.key_warps * p.column_warps;
+  auto smem = [&](int stages) {
+    return cb::q8_smem_bytes(a.head_dim, HB, warps, sp.column_blocks, a.dtype == CB_F32, stages, a.num_kv_heads);
+  };
+  const size_t fixed = smem(0), per = smem(1) - fixed;
   // each stage belongs to one producer and one key warp: whole multiples of both counts
   const int m = std::max(p.key_warps, cb::kQ8Producers);
   p.stages = (int)std::min<size_t>(cb::kQ8MaxStages, cb::kQ8RingBytes / per) / m * m;
