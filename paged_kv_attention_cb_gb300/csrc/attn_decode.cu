@@ -943,7 +943,8 @@ template <int D, int G>
 cudaError_t launch_dg(const DecodeArgs& p, const CUtensorMap& mk, const CUtensorMap& mv,
                       size_t smem, int hg, int num_requests, cudaStream_t s) {
   auto kern = decode_split_kernel<D, G>;
-  static bool attr_set = false;
+  static DeviceFlags attr_flags;
+  std::atomic<bool>& attr_set = device_flag(attr_flags);
   if (!attr_set) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kDecodeSmemLimit);

@@ -1230,7 +1230,8 @@ cudaError_t launch_d(const std::conditional_t<kShared, PrefixArgs, PrefillArgs>&
     if (err != cudaSuccess) return err;
   }
   auto kern = prefill_tile_kernel<D, kShared>;
-  static bool attr_set = false;
+  static DeviceFlags attr_flags;
+  std::atomic<bool>& attr_set = device_flag(attr_flags);
   constexpr size_t smem = smem_bytes<D>();
   if (!attr_set) {
     // the register split inside the kernel assumes kRegsLaunch registers per thread at

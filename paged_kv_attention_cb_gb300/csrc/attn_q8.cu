@@ -1066,8 +1066,14 @@ cudaError_t launch_split_t(const Q8Args& p, cudaStream_t s) {
       p.stages % p.key_warps != 0 || p.stages > kQ8MaxStages ||
       p.heads_per_cta * p.key_warps * p.column_warps > (NB == 1 ? 16 : 8))
     return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8SmemLimit);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  static DeviceFlags attr_flags;
+  std::atomic<bool>& attr_set = device_flag(attr_flags);
+  if (!attr_set) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kQ8SmemLimit);
+    if (e != cudaSuccess) return e;
+    attr_set = true;
+  }
   CUtensorMap mk, mv;
   e = cache_map(&mk, p.c.k, p.a, p.heads_per_cta);
   if (e == cudaSuccess) e = cache_map(&mv, p.c.v, p.a, p.heads_per_cta);

@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace cb {
 
 struct StepArgs {
@@ -78,6 +80,17 @@ cudaError_t launch_pdl(KernelId id, void (*kernel)(KArgs...), dim3 grid, dim3 bl
   return e;
 }
 
+
+// Kernel attributes are set per device, before the first launch there. The current device's flag
+// among `flags` -- set by the caller once its attributes are, so that two threads may both set
+// them but none launches without -- or a flag that stays false where there are too many devices.
+using DeviceFlags = std::atomic<bool>[64];
+inline std::atomic<bool>& device_flag(DeviceFlags& flags) {
+  static thread_local std::atomic<bool> none;
+  none = false;
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 ? flags[dev] : none;
+}
 
 cudaError_t launch_write_kv(const void* k_new, const void* v_new, void* k_cache, void* v_cache,
                             const int64_t* slot_mapping, int32_t num_tokens, int64_t num_slots,

@@ -37,11 +37,19 @@ CB_DEV void join(Acc& x, float m, float l, float4 o) {
 
 }  // namespace
 
-template <typename T>
-__global__ void __launch_bounds__(kMergeThreads) merge_rows_kernel(const MergeArgs m) {
+// The rows travel in the kernel arguments, so that the merge waits for no copy: few of them in a
+// small argument block (the copy of a large one costs a small step), many in few launches.
+template <int N>
+struct RowList {
+  MergeRow rows[N];
+};
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kMergeThreads)
+merge_rows_kernel(const MergeArgs m, const __grid_constant__ RowList<N> list) {
   __shared__ float4 sh_o[kMergeThreads];
   __shared__ float2 sh_ml[kMergeThreads];
-  const MergeRow& row = m.rows[blockIdx.x];
+  const MergeRow& row = list.rows[blockIdx.x];
   const int per = kMergeThreads / m.parts;  // outputs (of four values) per CTA
   const int part = threadIdx.x / per;
   const int f = blockIdx.y * per + threadIdx.x % per;
@@ -100,19 +108,31 @@ int merge_parts(int pieces) {
   return parts;
 }
 
-cudaError_t launch_merge(MergeArgs& m, const MergeRow* rows, int n, cudaStream_t stream) {
+namespace {
+
+template <int N>
+cudaError_t launch_rows(const MergeArgs& m, const MergeRow* rows, int n, cudaStream_t stream) {
   const int per = kMergeThreads / m.parts;
   const int F = m.num_q_heads * m.head_dim / 4;
-  for (int i = 0; i < n; i += kMergeRows) {
-    m.n = std::min(kMergeRows, n - i);
-    std::copy(rows + i, rows + i + m.n, m.rows);
-    const dim3 grid(m.n, (F + per - 1) / per);
+  for (int i = 0; i < n; i += N) {
+    const int k = std::min(N, n - i);
+    RowList<N> list;
+    std::copy(rows + i, rows + i + k, list.rows);
+    const dim3 grid(k, (F + per - 1) / per);
     const cudaError_t e =
-        m.dtype == 0 ? launch_pdl(kMergeRowsId, merge_rows_kernel<float>, grid, dim3(kMergeThreads), 0, stream, m)
-                     : launch_pdl(kMergeRowsId, merge_rows_kernel<__nv_bfloat16>, grid, dim3(kMergeThreads), 0, stream, m);
+        m.dtype == 0
+            ? launch_pdl(kMergeRowsId, merge_rows_kernel<float, N>, grid, dim3(kMergeThreads), 0, stream, m, list)
+            : launch_pdl(kMergeRowsId, merge_rows_kernel<__nv_bfloat16, N>, grid, dim3(kMergeThreads), 0, stream, m, list);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_merge(const MergeArgs& m, const MergeRow* rows, int n, cudaStream_t stream) {
+  if (n <= 64) return launch_rows<64>(m, rows, n, stream);
+  return launch_rows<1024>(m, rows, n, stream);
 }
 
 }  // namespace cb

@@ -15,7 +15,6 @@ struct MergeRow {
   int b, b_step, nb;
 };
 
-constexpr int kMergeRows = 128;     // rows per launch (they travel in the kernel arguments)
 constexpr int kMergeThreads = 256;
 
 struct MergeArgs {
@@ -25,13 +24,11 @@ struct MergeArgs {
   const float* part_o;   // [row][Hq][D] unnormalised
   const float2* part_ml; // [row][Hq] (running maximum in log2 units, sum)
   int parts;             // threads per output, each over a share of the pieces
-  int n;
-  MergeRow rows[kMergeRows];
 };
 
 // Threads per output for rows of up to `pieces` pieces.
 int merge_parts(int pieces);
 // `rows`: n rows, in as many launches as they need.
-cudaError_t launch_merge(MergeArgs& m, const MergeRow* rows, int n, cudaStream_t stream);
+cudaError_t launch_merge(const MergeArgs& m, const MergeRow* rows, int n, cudaStream_t stream);
 
 }  // namespace cb

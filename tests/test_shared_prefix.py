@@ -268,3 +268,56 @@ def test_binding_refuses():
     st.prefix = st.prefix + 8
     with pytest.raises(cb.CbError):
         st.run()
+
+
+@pytest.mark.gpu
+def test_samples_of_one_prompt_step_by_step():
+    """A prompt is prefilled once; five requests share its whole blocks and decode tokens of their
+    own, each step writing its rows and attending the prompt and what came before."""
+    rng = torch.Generator().manual_seed(3)
+    Hq, Hkv, D, BS, n, prompt, steps = 16, 4, 128, 16, 5, 200, 4
+    shared = prompt // BS * BS  # the partial block is each request's own
+    per = -(-(prompt + steps) // BS)
+    nb = 2 + shared // BS + n * (per - shared // BS)
+    rows = lambda *s: torch.randn(s, generator=rng).bfloat16()
+    k_cache, v_cache = rows(nb, BS, Hkv, D).cuda(), rows(nb, BS, Hkv, D).cuda()
+    perm = np.random.default_rng(1).permutation(np.arange(2, nb))
+    table = np.zeros((n, per), np.int32)
+    table[:, : shared // BS] = perm[: shared // BS]
+    table[:, shared // BS:] = perm[shared // BS:].reshape(n, -1)
+    slot = lambda r, p: table[r, p // BS].astype(np.int64) * BS + p % BS
+    pk, pv = rows(prompt, Hkv, D), rows(prompt, Hkv, D)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()
+    # the prompt: one prefill step of request 0, then the tail block's rows for the others
+    qsl, seq = np.array([0, prompt], np.int32), np.array([prompt], np.int32)
+    q0 = rows(prompt, Hq, D).cuda()
+    cb.paged_attention(torch.empty_like(q0), q0, k_cache, v_cache, dev(qsl), dev(seq), dev(table[:1]), qsl, seq,
+                       cb.alloc_workspace(1, prompt, Hq, Hkv, D), k_new=pk.cuda(), v_new=pv.cuda(),
+                       slot_mapping=dev(slot(0, np.arange(prompt))))
+    tail = np.arange(shared, prompt)
+    for r in range(1, n):
+        cb.write_kv(pk[shared:].cuda(), pv[shared:].cuda(), k_cache, v_cache, dev(slot(r, tail)))
+    ws = cb.alloc_workspace_shared(n, n, Hq, Hkv, D)
+    plen = np.full(n, shared, np.int32)
+    group = np.array([0, n], np.int32)
+    mine = [([pk], [pv]) for _ in range(n)]
+    for i in range(steps):
+        q, k, v = rows(n, Hq, D), rows(n, Hkv, D), rows(n, Hkv, D)
+        qsl, seq = np.arange(n + 1, dtype=np.int32), np.full(n, prompt + i + 1, np.int32)
+        out = torch.empty((n, Hq, D), dtype=torch.bfloat16, device="cuda")
+        cb.paged_attention_shared(out, q.cuda(), k_cache, v_cache, dev(qsl), dev(seq), dev(table), dev(plen), qsl,
+                                  seq, plen, group, ws, k_new=k.cuda(), v_new=v.cuda(),
+                                  slot_mapping=dev(np.array([slot(r, np.int64(prompt + i)) for r in range(n)])),
+                                  flags=cb.CB_FLAG_SHARE_ALWAYS)
+        for r in range(n):
+            mine[r][0].append(k[r:r + 1])
+            mine[r][1].append(v[r:r + 1])
+            K, V = (torch.cat(x).double().numpy() for x in mine[r])
+            for g in range(Hkv):
+                heads = slice(4 * g, 4 * g + 4)
+                ref = oracle.paged_kv.softmax_attend(q[r, heads].double().numpy(), K[:, g], V[:, g], D ** -0.5)
+                absv = oracle.paged_kv.softmax_attend(q[r, heads].double().numpy(), K[:, g], np.abs(V[:, g]), D ** -0.5)
+                got = out[r, heads].double().cpu().numpy()
+                # bf16 outputs and weights: 2^-8 of the value and of the mean |V|; scores 2^-15 B, B < 2^6 here
+                assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -9) * absv).all()
+    assert cb.read_error_word(ws) == 0
