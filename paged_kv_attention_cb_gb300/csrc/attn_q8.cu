@@ -18,9 +18,10 @@
 //   Each warp's share of an item in a CTA (a piece) becomes a partial row that the merge kernel
 //   joins (merge.h); only an item that one warp per head has to itself is written directly.
 // * Staging. Producer warps bring each block (16 keys, up to 8 KV heads, K and V) with two
-//   swizzled tensor copies and its scales with two bulk copies into a ring of stages. Four of
-//   them, taking the blocks in turn: one warp needs ~0.5 us to place and issue a block, which
-//   bounded everything but the widest rows (64 x 32768 with one KV head: 1.2 TB/s).
+//   swizzled tensor copies, and its scales with two bulk copies, into a ring of stages. One
+//   warp needs ~0.5 us to place and issue a block, which bounded everything but the widest
+//   rows: four warps take the blocks in turn, and where blocks are small several lanes of
+//   each a block of their own at once.
 // * Operands. e4m3 is exact in fp16, so the contractions are fp16 mma.sync with fp32
 //   accumulation, and the conversion is one instruction per pair (cvt.f16x2.e4m3x2). q is
 //   scaled per row by a power of two to a largest magnitude in [2^13, 2^14): a bf16 row is
@@ -272,12 +273,13 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
   allow_dependent_launch();
   __syncthreads();
 
+  const int GB = p.group_blocks;  // a power of two
   const int producer = warp - nwarps;
   int issued_blocks = 0;  // producers: one past the last block whose copies this warp issued
   if (producer >= 0) {
     // =================================================== producer warps
-    // All walk the same pieces; block i is issued by warp i % kQ8Producers, and the first also
-    // hands the pieces to the consumers.
+    // All walk the same pieces; block i is issued by warp i / GB % kQ8Producers, lanes of it the GB
+    // blocks of a group together, and the first also hands the pieces to the consumers.
     const int u_lo = p.start[b].u, u_hi = p.start[b + 1].u;
     const uint64_t policy = l2_policy_evict_first();  // the stream is read once
     const int BS = p.a.block_size;
@@ -328,6 +330,24 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       return lane < n ? __ldg(p.a.block_table + (long long)rr * p.a.bt_stride +
                               ((kb + lane) * kKB >> p.lg_block))
                       : 0;
+    };
+    // one lane: the copies of key block kb, in page pg, into stage st_i
+    auto copy_block = [&](int kb, int pg, int st_i) {
+      const int key0 = (kb * kKB) & (BS - 1);
+      uint64_t* const full = &sm.full[st_i];
+      uint8_t* st = stages + st_i * stage_bytes;
+      uint8_t* sc = scales + st_i * 2 * scale_bytes;
+      const bool page_ok = pg >= 0 && pg < p.a.num_blocks;
+      if (!page_ok) record_error(p.a.error_word, CB_DEVERR_BLOCK_ID);
+      mbar_arrive_expect_tx(full, (uint32_t)(stage_bytes + (page_ok ? 2 * scale_bytes : 0)));
+      const int page = page_ok ? pg : p.a.num_blocks;  // past the pool: zeros
+      tma_load_4d_hint(st, &tmap_k, full, 0, key0, hg * HB, page, policy);
+      tma_load_4d_hint(st + box_bytes, &tmap_v, full, 0, key0, hg * HB, page, policy);
+      if (page_ok) {
+        const long long at = (((long long)pg << p.lg_block) + key0) * Hkv;
+        bulk_load(sc, p.c.k_scale + at, (uint32_t)scale_bytes, full);
+        bulk_load(sc + scale_bytes, p.c.v_scale + at, (uint32_t)scale_bytes, full);
+      }
     };
     bool more = u_lo < u_hi;
     int kb0 = 0, kb1 = 0, pages = 0;
@@ -391,36 +411,41 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       for (int kb_base = first; kb_base < last && ok; kb_base += 32) {
         const int n = min(32, last - kb_base);
         const int cur = pages;
-        for (int j = 0; j < n; ++j) {
-          if (i % kQ8Producers == producer) {
-            const int pg = __shfl_sync(0xffffffffu, cur, j);
-            if ((round > 0 &&
-                 !mbar_wait_warp_or_abort(&sm.empty[s], (uint32_t)(round - 1) & 1, &sm.abort_flag)) ||
-                *reinterpret_cast<volatile int*>(&sm.abort_flag)) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) {
-              const int key0 = ((kb_base + j) * kKB) & (BS - 1);
-              uint8_t* st = stages + s * stage_bytes;
-              uint8_t* sc = scales + s * 2 * scale_bytes;
-              const bool page_ok = pg >= 0 && pg < p.a.num_blocks;
-              if (!page_ok) record_error(p.a.error_word, CB_DEVERR_BLOCK_ID);
-              mbar_arrive_expect_tx(&sm.full[s], (uint32_t)(stage_bytes + (page_ok ? 2 * scale_bytes : 0)));
-              const int page = page_ok ? pg : p.a.num_blocks;  // past the pool: zeros
-              tma_load_4d_hint(st, &tmap_k, &sm.full[s], 0, key0, hg * HB, page, policy);
-              tma_load_4d_hint(st + box_bytes, &tmap_v, &sm.full[s], 0, key0, hg * HB, page, policy);
-              if (page_ok) {
-                const long long at = (((long long)pg << p.lg_block) + key0) * Hkv;
-                bulk_load(sc, p.c.k_scale + at, (uint32_t)scale_bytes, &sm.full[s]);
-                bulk_load(sc + scale_bytes, p.c.v_scale + at, (uint32_t)scale_bytes, &sm.full[s]);
+        for (int j = 0, cnt; j < n; j += cnt) {
+          if (GB == 1) {
+            cnt = 1;
+            if ((i & (kQ8Producers - 1)) == producer) {
+              const int pg = __shfl_sync(0xffffffffu, cur, j);
+              if ((round > 0 &&
+                   !mbar_wait_warp_or_abort(&sm.empty[s], (uint32_t)(round - 1) & 1, &sm.abort_flag)) ||
+                  *reinterpret_cast<volatile int*>(&sm.abort_flag)) {
+                ok = false;
+                break;
               }
+              if (lane == 0) copy_block(kb_base + j, pg, s);
+              __syncwarp();
+              issued_blocks = i + 1;
             }
-            __syncwarp();
-            issued_blocks = i + 1;
+          } else {
+            cnt = min(GB - (i & (GB - 1)), n - j);  // blocks of this group
+            if ((i / GB & (kQ8Producers - 1)) == producer) {
+              // lane l < cnt: block j + l, stage s + l
+              const int pg = __shfl_sync(0xffffffffu, cur, (j + lane) & 31);
+              const bool mine = lane < cnt;
+              const bool free = !mine || round == 0 ||
+                                mbar_wait_or_abort(&sm.empty[s + lane], (uint32_t)(round - 1) & 1, &sm.abort_flag);
+              if (!__all_sync(0xffffffffu, free && *reinterpret_cast<volatile int*>(&sm.abort_flag) == 0)) {
+                ok = false;
+                break;
+              }
+              if (mine) copy_block(kb_base + j + lane, pg, s + lane);
+              __syncwarp();
+              issued_blocks = i + cnt;
+            }
           }
-          ++i;
-          if (++s == p.stages) {
+          i += cnt;
+          s += cnt;
+          if (s == p.stages) {
             s = 0;
             ++round;
           }
@@ -590,9 +615,16 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if constexpr (F32) return __uint_as_float(raw[e]);
             return __uint_as_float(e & 1 ? raw[e / 2] & 0xffff0000u : raw[e / 2] << 16);
           };
+          // bits of the row's largest magnitude (a row with an infinity or a NaN gives NaNs anyway)
           uint32_t top = 0u;
+          if constexpr (F32) {
 #pragma unroll
-          for (int e = 0; e < D / 4; ++e) top = max(top, finite_magnitude(value(e)));
+            for (int e = 0; e < kRaw; ++e) top = max(top, raw[e] & 0x7fffffffu);
+          } else {
+#pragma unroll
+            for (int e = 0; e < kRaw; ++e) top = __vmaxu2(top, raw[e] & 0x7fff7fffu);
+            top = max(top & 0xffff0000u, top << 16);
+          }
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
           const int ex = top == 0u ? 13 : max((int)(top >> 23) - 127, -100);
@@ -708,12 +740,11 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
               if constexpr (F32) sa[nb][e] += sc_[2][nb][e];
             }
           // ---- scales: 2^ek on the score, ev in the weight's exponent
-          const float fa = e8m0_value(lds_u8(sc + key_a * Hkv));
-          const float fb = e8m0_value(lds_u8(sc + (key_a + 8) * Hkv));
-          const int ca = lds_u8(sc + scale_bytes + key_a * Hkv);
-          const int cb_ = lds_u8(sc + scale_bytes + (key_a + 8) * Hkv);
-          const float ea = ca == 255 ? __uint_as_float(0x7fc00000u) : (float)(ca - kE8m0Bias);
-          const float eb = cb_ == 255 ? __uint_as_float(0x7fc00000u) : (float)(cb_ - kE8m0Bias);
+          // (scale bytes 1 .. 254: the exponent field of a normal float)
+          const float fa = __uint_as_float((uint32_t)lds_u8(sc + key_a * Hkv) << 23);
+          const float fb = __uint_as_float((uint32_t)lds_u8(sc + (key_a + 8) * Hkv) << 23);
+          const float ea = (float)(lds_u8(sc + scale_bytes + key_a * Hkv) - kE8m0Bias);
+          const float eb = (float)(lds_u8(sc + scale_bytes + (key_a + 8) * Hkv) - kE8m0Bias);
           const bool edge = key_base < inner_lo || key_base + kKB - 1 > inner_hi;  // warp-uniform
           uint32_t pw[NB][2 * kSplit];
 #pragma unroll
@@ -933,8 +964,9 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
   __syncthreads();
   // (Each producer waits for its own blocks among the latest of every stage that it knows of.)
   if (producer >= 0 && lane == 0 && *reinterpret_cast<volatile int*>(&sm.abort_flag)) {
-    for (int j = issued_blocks - 1; j >= 0 && j >= issued_blocks - p.stages; j -= kQ8Producers)
-      mbar_wait(&sm.full[j % p.stages], (uint32_t)(j / p.stages) & 1);
+    for (int j = issued_blocks - 1; j >= 0 && j >= issued_blocks - p.stages; --j)
+      if ((j / GB & (kQ8Producers - 1)) == producer)
+        mbar_wait(&sm.full[j % p.stages], (uint32_t)(j / p.stages) & 1);
   }
 }
 
@@ -1059,12 +1091,13 @@ cudaError_t cache_map(CUtensorMap* map, void* cache, const StepArgs& a, int hb) 
 template <int D, int NB, bool F32>
 cudaError_t launch_split_t(const Q8Args& p, cudaStream_t s) {
   auto kern = q8_split_kernel<D, NB, F32>;
-  const size_t smem = q8_smem_bytes(D, p.heads_per_cta, p.heads_per_cta * p.key_warps * p.column_warps, NB, F32,
-                                    p.stages, p.a.num_kv_heads);
+  const int warps = p.heads_per_cta * p.key_warps * p.column_warps;
+  const size_t smem = q8_smem_bytes(D, p.heads_per_cta, warps, NB, F32, p.stages, p.a.num_kv_heads);
   // a stage belongs to one producer and one key warp, which see every one of its phases
-  if (smem > (size_t)kQ8SmemLimit || p.stages < kQ8Producers || p.stages % kQ8Producers != 0 ||
-      p.stages % p.key_warps != 0 || p.stages > kQ8MaxStages ||
-      p.heads_per_cta * p.key_warps * p.column_warps > (NB == 1 ? 16 : 8))
+  const int gb = p.group_blocks;
+  if (smem > (size_t)kQ8SmemLimit || gb < 1 || gb > 32 || (gb & (gb - 1)) != 0 || p.stages > kQ8MaxStages ||
+      p.stages < gb * kQ8Producers || p.stages % (gb * kQ8Producers) != 0 || p.stages % p.key_warps != 0 ||
+      warps > (NB == 1 ? 16 : 8))
     return cudaErrorInvalidValue;
   cudaError_t e = cudaSuccess;
   static DeviceFlags attr_flags;
@@ -1079,7 +1112,7 @@ cudaError_t launch_split_t(const Q8Args& p, cudaStream_t s) {
   if (e == cudaSuccess) e = cache_map(&mv, p.c.v, p.a, p.heads_per_cta);
   if (e != cudaSuccess) return e;
   return launch_pdl(kDecodeQ8, kern, dim3(p.num_ctas, p.a.num_kv_heads / p.heads_per_cta),
-                    dim3((p.heads_per_cta * p.key_warps * p.column_warps + kQ8Producers) * 32), smem, s,
+                    dim3((warps + kQ8Producers) * 32), smem, s,
                     mk, mv, p);
 }
 

@@ -33,7 +33,7 @@ cudaError_t launch_read_kv_q8(void* k_out, void* v_out, const Q8Cache& c,
 constexpr int kQ8KeyBlock = 16;      // keys per unit of work (and per stage of the ring)
 constexpr int kQ8MaxStages = 32;
 constexpr int kQ8MaxHeads = 8;       // KV heads per CTA
-constexpr int kQ8Producers = 4;      // producer warps per CTA
+constexpr int kQ8Producers = 4;      // producer warps per CTA (a power of two)
 constexpr int kQ8MaxColumnWarps = 4; // warps of a head on different columns
 constexpr int kQ8TableCtas = 192;    // CTAs per group of heads (their starts are arguments)
 constexpr int kQ8SmemLimit = 232448; // 227 KiB dynamic shared memory per CTA
@@ -60,7 +60,9 @@ struct Q8Args {
   int heads_per_cta;  // HB
   int key_warps;      // KW: warps per KV head and columns; block i goes to those with i % KW
   int column_warps;   // CW: warps per KV head and block, each with 8 NB of the item's columns
-  int stages;         // multiple of KW and of kQ8Producers
+  int group_blocks;   // GB: blocks that a producer's lanes issue together (a power of two); block
+                      // i belongs to producer i / GB % kQ8Producers
+  int stages;         // multiple of KW and of GB * kQ8Producers
   int tile_tokens;    // TT: query tokens per item (TT * G columns, at most 8 NB CW)
   int lg_block;       // log2 of block_size
   int lg_group;       // log2 of query heads per KV head

@@ -125,20 +125,7 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
   while ((1 << p.lg_block) < a.block_size) ++p.lg_block;
   const int HB = p.heads_per_cta = sp.heads;
   p.column_warps = sp.column_warps;
-  p.key_warps = sp.key_warps;
-  const int warps = HB * p.key_warps * p.column_warps;
-  auto smem = [&](int stages) {
-    return cb::q8_smem_bytes(a.head_dim, HB, warps, sp.column_blocks, a.dtype == CB_F32, stages, a.num_kv_heads);
-  };
-  const size_t fixed = smem(0), per = smem(1) - fixed;
-  // each stage belongs to one producer and one key warp: whole multiples of both counts
-  const int m = std::max(p.key_warps, cb::kQ8Producers);
-  p.stages = (int)std::min<size_t>(cb::kQ8MaxStages, cb::kQ8RingBytes / per) / m * m;
-  if (p.stages * per < cb::kQ8RingBytes * 3 / 4 && p.stages + m <= cb::kQ8MaxStages &&
-      fixed + (p.stages + m) * per <= (size_t)cb::kQ8SmemLimit)
-    p.stages += m;
-
-  const int TT = p.tile_tokens, KW = p.key_warps, W = a.sliding_window;
+  const int TT = p.tile_tokens, W = a.sliding_window;
   auto blocks = [&](int pos0, int ntok) {
     return (pos0 + ntok - 1) / cb::kQ8KeyBlock - first_key(pos0, W) / cb::kQ8KeyBlock + 1;
   };
@@ -158,6 +145,25 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
   const int groups = a.num_kv_heads / HB;
   long long C = std::max(1, std::min(cb::sm_count(), cb::kQ8TableCtas) / groups);
   C = std::min(C, (U + cb::kQ8MinBlocksPerCta - 1) / cb::kQ8MinBlocksPerCta);
+
+  // fewer key warps (and partial rows) where each would have less than four blocks of a CTA's
+  p.key_warps = sp.key_warps;
+  while (p.key_warps > 2 && U < 4 * C * p.key_warps) p.key_warps /= 2;
+  const int KW = p.key_warps;
+  const int warps = HB * p.key_warps * p.column_warps;
+  auto smem = [&](int stages) {
+    return cb::q8_smem_bytes(a.head_dim, HB, warps, sp.column_blocks, a.dtype == CB_F32, stages, a.num_kv_heads);
+  };
+  const size_t fixed = smem(0), per = smem(1) - fixed;
+  // each stage belongs to one producer and one key warp: whole multiples of both counts
+  int m = std::max(p.key_warps, cb::kQ8Producers);
+  p.stages = (int)std::min<size_t>(cb::kQ8MaxStages, cb::kQ8RingBytes / per) / m * m;
+  if (p.stages * per < cb::kQ8RingBytes * 3 / 4 && p.stages + m <= cb::kQ8MaxStages &&
+      fixed + (p.stages + m) * per <= (size_t)cb::kQ8SmemLimit)
+    p.stages += m;
+  // rings of many small blocks: groups of them, two groups per producer in the ring at least
+  p.group_blocks = 1;
+  while (p.group_blocks < 4 && p.stages % (4 * p.group_blocks * cb::kQ8Producers) == 0) p.group_blocks *= 2;
 
   // ---- the partition: CTAs are filled in order up to a load, the blocks they read and
   // kPieceBlocks for each piece they have; the least load (to a block) that C CTAs take
@@ -388,7 +394,9 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
   a.error_word = static_cast<int32_t*>(workspace);
 
   // a 16-key block lies in one page from block_size 16 on; the rest runs on the portable kernel
-  const bool fast = block_size % cb::kQ8KeyBlock == 0 && !(flags & CB_FLAG_PORTABLE_ONLY);
+  // (which also takes head counts whose blocks' scales would fill the ring)
+  const bool fast = block_size % cb::kQ8KeyBlock == 0 && num_kv_heads <= 128 &&
+                    !(flags & CB_FLAG_PORTABLE_ONLY);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   static thread_local Q8Plan plan;  // its vectors keep their storage from call to call
