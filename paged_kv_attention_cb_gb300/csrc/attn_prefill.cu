@@ -103,6 +103,7 @@ struct UnitDesc {
 // tiles' key ranges is walked in key tiles kt0 .. kt0 + nkt - 1.
 struct Geo {
   int r, g, q_start, q_len, seq, ctx, qt0, has_b, tok0, tok_end, kt0, nkt;
+  bool split_all;  // split units: the pair's keys are this one unit
 };
 
 CB_DEV Geo geo_of(int r, int q_start, int q_len, int seq_len, int g, int pair, int TQ, int W) {
@@ -187,15 +188,14 @@ CB_DEV Work work_of(const PrefillArgs& p, int cta) {
   return Work{-1, 0, 0};
 }
 
-// Shared-prefix units: index -> (entry, KV head, pair of query tiles, split of the key tiles),
-// the pairs that read the same keys next to each other. `pair` carries the split above bit 16.
+// Split units: index -> (entry, KV head, pair of query tiles, split of the key tiles), the pairs
+// that read the same keys next to each other. `pair` carries the split above bit 16.
 CB_DEV Work work_of(const PrefixArgs& p, int cta) {
   const int Hkv = p.a.num_kv_heads;
   int base = 0;
   for (int e = 0; e < p.n_entries; ++e) {
     const int npairs = (p.entries[e].n_qtiles + 1) / 2;
-    const int splits = (((p.entries[e].seq_len + kKeys - 1) / kKeys) + p.tiles_per_unit - 1) / p.tiles_per_unit;
-    const int n = npairs * Hkv * splits;
+    const int n = npairs * Hkv * p.splits[e];
     if (cta < base + n) {
       const int k = cta - base;
       return Work{e, k / npairs % Hkv, k % npairs | (k / (npairs * Hkv)) << 16};
@@ -205,22 +205,21 @@ CB_DEV Work work_of(const PrefixArgs& p, int cta) {
   return Work{-1, 0, 0};
 }
 
-// A shared-prefix unit (its descriptor's r is the entry): the prefix as a context without new
-// tokens, so that every row attends all of it, and of its key tiles those of the unit's split.
-CB_DEV Geo geo_of(const PrefixArgs& p, const UnitDesc& d, int TQ) {
-  Geo e;
-  e.r = p.entries[d.r].r;
-  e.g = d.g;
-  e.q_start = d.q_start;
-  e.q_len = d.q_len;
-  e.seq = d.seq_len;
-  e.ctx = d.seq_len;
-  e.qt0 = kTiles * (d.pair & 0xffff);
-  e.has_b = e.qt0 + 1 < (d.q_len + TQ - 1) / TQ;
-  e.tok0 = e.qt0 * TQ;
-  e.tok_end = min(d.q_len, e.tok0 + kTiles * TQ);
-  e.kt0 = (d.pair >> 16) * p.tiles_per_unit;
-  e.nkt = min(p.tiles_per_unit, (d.seq_len + kKeys - 1) / kKeys - e.kt0);
+// A split unit (its descriptor's r is the entry): of its pair's key tiles those of the unit's split
+// (none: nkt <= 0). A shared prefix is a context without new tokens, so that every row attends all
+// of it.
+template <bool kCausal>
+CB_DEV Geo split_geo(const PrefixArgs& p, const UnitDesc& d, int TQ, int W) {
+  const int ctx = kCausal ? d.seq_len - d.q_len : d.seq_len;
+  Geo e = geo_of(p.entries[d.r].r, d.q_start, d.q_len, ctx + d.q_len, d.g, d.pair & 0xffff, TQ, W);
+  if (!kCausal) {
+    e.seq = d.seq_len;
+    e.nkt = (d.seq_len + kKeys - 1) / kKeys;
+  }
+  const int first = (d.pair >> 16) * p.tiles_per_unit;
+  e.split_all = first == 0 && e.nkt <= p.tiles_per_unit;
+  e.kt0 += first;
+  e.nkt = min(p.tiles_per_unit, e.nkt - first);
   return e;
 }
 
@@ -311,15 +310,21 @@ __device__ __noinline__ void copy_rows(uint8_t* dst, unsigned gen, int ids_cur, 
 
 }  // namespace
 
-// kShared: over the shared prefixes of groups of decode rows (PrefixArgs), into partial rows.
-template <int D, bool kShared>
+// Whole pairs (PrefillArgs), or pairs whose keys are split into units (PrefixArgs): chunks, or a
+// prefix that the rows of a group share. The two kinds of split are instances of their own: with the
+// direct output of undivided pairs beside it, the prefix tiles took 275 instead of 245 us on four
+// groups of 37 rows before 32768 positions.
+enum Pairs { kWholePairs, kSplitChunks, kSharedPrefix };
+
+template <int D, Pairs kPairs>
 __global__ void __launch_bounds__(kThreadsBound, 1)
 prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v,
                     const __grid_constant__ CUtensorMap tmap_kn,
                     const __grid_constant__ CUtensorMap tmap_vn,
                     const __grid_constant__ CUtensorMap tmap_q,
-                    const __grid_constant__ std::conditional_t<kShared, PrefixArgs, PrefillArgs> p) {
+                    const __grid_constant__ std::conditional_t<kPairs != kWholePairs, PrefixArgs, PrefillArgs> p) {
+  constexpr bool kSplit = kPairs != kWholePairs;
   static_assert(D == 64 || D == 128, "head_dim");
   constexpr int kHalves = D / 64;
   constexpr int kTile = tile_bytes<D>();
@@ -342,7 +347,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
   // Graph replays: the one unit of this CTA, found with a block scan over the device
   // metadata (request order; each request with q_len > 1 has ceil(n_qtiles / 2) * Hkv).
   __shared__ UnitDesc s_first;  // the unit found on the device (kept out of registers)
-  if (!kShared && p.device_work) {
+  if (!kSplit && p.device_work) {
     grid_dependency_wait();
     __shared__ int s_tot[kThreads / 32];
     __shared__ int s_hit[2];
@@ -471,7 +476,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
   // that a CTA takes a new unit as soon as it can (and CTAs that start late, on SMs a
   // decode grid held, take what is left).
   auto unit_geo = [&](const UnitDesc& d) -> Geo {
-    if constexpr (kShared) return geo_of(p, d, TQ);
+    if constexpr (kSplit) return split_geo<kPairs == kSplitChunks>(p, d, TQ, W);
     else return geo_of(d, TQ, W);
   };
   auto read_unit = [&](int u, UnitDesc& d) -> bool {
@@ -523,17 +528,21 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
           // claimed once the previous unit's loads are all issued (the ring's depth
           // ahead of its products), so that a unit goes to the first CTA that can
           // start it: claimed earlier, a light unit could wait behind a heavy one
-          int idx = 0;
-          if (lane == 0) idx = atomicAdd(p.unit_counter, 1);
-          idx = __shfl_sync(0xffffffffu, idx, 0);
-          d = UnitDesc{-1, 0, 0, 0, 0, 0, 0};
-          if (idx < p.total_units) {
-            const Work w = work_of(p, idx);
-            if (w.e >= 0) {
-              const PrefillEntry& en = p.entries[w.e];
-              d = UnitDesc{kShared ? w.e : en.r, en.q_start, en.q_len, en.seq_len, w.g, w.pair, 1};
+          bool empty = false;
+          do {
+            int idx = 0;
+            if (lane == 0) idx = atomicAdd(p.unit_counter, 1);
+            idx = __shfl_sync(0xffffffffu, idx, 0);
+            d = UnitDesc{-1, 0, 0, 0, 0, 0, 0};
+            if (idx < p.total_units) {
+              const Work w = work_of(p, idx);
+              if (w.e >= 0) {
+                const PrefillEntry& en = p.entries[w.e];
+                d = UnitDesc{kSplit ? w.e : en.r, en.q_start, en.q_len, en.seq_len, w.g, w.pair, 1};
+              }
             }
-          }
+            if constexpr (kPairs == kSplitChunks) empty = d.live && unit_geo(d).nkt <= 0;  // past its pair's keys
+          } while (empty);
         }
         if (lane == 0) {
           bar.unit[u & 1] = d;
@@ -711,7 +720,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
       uint64_t dq = dQ + (uint64_t)(t * (kTile >> 4));
       uint64_t dk = dK + (uint64_t)((i % kStages) * (kTile >> 4));
       uint32_t id = idS;
-      if constexpr (kShared) {
+      if constexpr (kSplit) {
         if (halves) {
           dq = dQ;
           dk += (uint64_t)(t * ((kKeys / 2 * 128) >> 4));
@@ -728,7 +737,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
     // O_t += P_t V with P in the first columns of S_t and V in ring slot i
     auto pv = [&](int t, int i, bool acc) {
       const uint64_t dv = dV + (uint64_t)((i % kStages) * (kTile >> 4));
-      if constexpr (kShared) {
+      if constexpr (kSplit) {
         if (halves) {
 #pragma unroll
           for (int ks = 0; ks < kKeys / 32; ++ks)
@@ -755,7 +764,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
       if (!d.live) break;
       const Geo e = unit_geo(d);
       const int nkt = e.nkt;
-      if constexpr (kShared) halves = !e.has_b;
+      if constexpr (kSplit) halves = !e.has_b;
       const bool has_b = e.has_b || halves;  // group B has work
       ok = mbar_wait_warp_or_abort(&bar.q_full, (uint32_t)(u & 1), &bar.abort) && slot_ready(i_base);
       if (!ok) break;
@@ -826,7 +835,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const uint32_t tO = tmem + lane_addr + 2 * kKeys + t * D;
     int i_base = 0;
     int swaits = 0;  // s_full[t] waits so far (phase parity)
-    const bool copy_rows_after = !kShared && p.k_new != nullptr && !p.device_work;  // the row copy below
+    const bool copy_rows_after = !kSplit && p.k_new != nullptr && !p.device_work;  // the row copy below
     bool claimed = false;  // its first part is claimed already (lane 0: first_part)
     int first_part = 0;
     int owaits = 0;  // o_done[t] waits so far
@@ -856,7 +865,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
       {
         const Geo e = CB_UNIT_GEO();
         const int unit_nkt = e.nkt;
-        const bool tile_live = t == 0 || e.has_b || kShared;
+        const bool tile_live = t == 0 || e.has_b || kSplit;
         if (!tile_live) {  // this unit has no tile B
           i_base += 2 * unit_nkt;
           CB_RELEASE_UNIT();
@@ -865,8 +874,8 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         kt0 = e.kt0;
         nkt = e.nkt;
         seq = e.seq;
-        if constexpr (kShared) both = e.has_b;
-        const int tok0 = (e.qt0 + (kShared && !e.has_b ? 0 : t)) * TQ;
+        if constexpr (kSplit) both = e.has_b;
+        const int tok0 = (e.qt0 + (kSplit && !e.has_b ? 0 : t)) * TQ;
         const int qpos = e.ctx + tok0 + row / G;
         max_kv = min(qpos, e.seq - 1);
         min_kv = W > 0 ? max(0, qpos - W + 1) : 0;
@@ -981,8 +990,8 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[t]);
       };
-      if (kShared && !both) {
-        if constexpr (kShared)
+      if (kSplit && !both) {
+        if constexpr (kSplit)
           for (int j = 0; j < nkt && ok; ++j)
             key_tile(std::integral_constant<int, kKeys / 2>{}, j, t * (kKeys / 2));
       } else {
@@ -991,17 +1000,21 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
       // ---- epilogue: O / l for the rows of this tile. The rows' output offsets are
       // computed while the last PV product runs (~600 cycles after the wait otherwise).
       const int q4 = lane & 3;
+      bool partial = kSplit;  // the unit's rows are joined with others' by the merge
       long long orow[4];  // output offset of rows 4a .. 4a + 3 of the warp, -1 past q_len
       {
         const Geo e = CB_UNIT_GEO();
+        if constexpr (kPairs == kSplitChunks) partial = !(both && e.split_all);
         const int lg = __ffs(G) - 1;
 #pragma unroll
         for (int s4 = 0; s4 < 4; ++s4) {
           const int r = (warp & 3) * 32 + 4 * (lane >> 2) + s4;  // tile row
-          const int tok = (e.qt0 + (kShared && !both ? 0 : t)) * TQ + (r >> lg);
-          if constexpr (kShared) {  // offset in the partial rows, four fp32 pieces a line
-            const long long pr = partial_row(p, ud->r, ud->pair >> 16, t, both, e.tok0, tok);
-            orow[s4] = tok < e.q_len ? (pr * p.a.num_q_heads + e.g * G + (r & (G - 1))) * D + q4 * 8 : -1;
+          const int tok = (e.qt0 + (kSplit && !both ? 0 : t)) * TQ + (r >> lg);
+          if (partial) {  // offset in the partial rows, four fp32 pieces a line
+            if constexpr (kSplit) {
+              const long long pr = partial_row(p, ud->r, ud->pair >> 16, t, both, e.tok0, tok);
+              orow[s4] = tok < e.q_len ? (pr * p.a.num_q_heads + e.g * G + (r & (G - 1))) * D + q4 * 8 : -1;
+            }
           } else {
             orow[s4] = tok < e.q_len ? ((long long)(e.q_start + tok) * p.a.num_q_heads + e.g * G +
                                         (r & (G - 1))) * D + q4 * 16
@@ -1025,63 +1038,66 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         ok = false;
       if (ok) {
         tcgen05_fence_after();
-        if constexpr (kShared) {
-          // the unnormalised O and the row's statistics, as fp32 partial rows: the same in-quad
-          // transpose of 32-byte pieces, 32 columns (one 128-byte line) at a time
+        if constexpr (kSplit) {
+          if (partial) {
+            // the unnormalised O and the row's statistics, as fp32 partial rows: the same in-quad
+            // transpose of 32-byte pieces, 32 columns (one 128-byte line) at a time
 #pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t w[32];
-            tmem_ld32(tO + c0, w);
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t w[32];
+              tmem_ld32(tO + c0, w);
+              tmem_wait_ld();
+              quad_transpose(w, lane);
+#pragma unroll
+              for (int s4 = 0; s4 < 4; ++s4) {
+                if (orow[s4] < 0) continue;
+                st_global_v8(p.part_o + orow[s4] + c0, w[8 * s4 + 0], w[8 * s4 + 1], w[8 * s4 + 2], w[8 * s4 + 3],
+                             w[8 * s4 + 4], w[8 * s4 + 5], w[8 * s4 + 6], w[8 * s4 + 7]);
+              }
+            }
+            const int tok0 = kTiles * (ud->pair & 0xffff) * TQ;
+            const int tok = tok0 + (both ? t : 0) * TQ + row / G;
+            if (tok < ud->q_len)
+              p.part_ml[partial_row(p, ud->r, ud->pair >> 16, t, both, tok0, tok) * p.a.num_q_heads +
+                        ud->g * G + (row & (G - 1))] = make_float2(m_ref, l);
+          }
+        }
+        if (!partial) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          // O / l as bf16 in whole 128-byte lines. Each lane holds its own row (TMEM lane =
+          // row); a transpose of 32-byte pieces within each group of four lanes gives lane
+          // 4a + q piece q of rows 4a .. 4a + 3 of the warp, so that one store instruction
+          // writes 8 rows x 128 contiguous bytes instead of 32 rows x 16 bytes (the stores of
+          // one row per lane kept the LSU busy ~4000 cycles per unit).
+          const bool wide = (reinterpret_cast<uintptr_t>(p.a.out) & 31) == 0;
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out);
+#pragma unroll
+          for (int c0 = 0; c0 < D; c0 += 64) {
+            uint32_t o0[32], o1[32];
+            tmem_ld32(tO + c0, o0);
+            tmem_ld32(tO + c0 + 32, o1);
             tmem_wait_ld();
+            uint32_t w[32];  // piece k = words 8k .. 8k + 7 = columns c0 + 16k .. c0 + 16k + 15
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              w[i] = pack_bf16x2(__uint_as_float(o0[2 * i]) * inv, __uint_as_float(o0[2 * i + 1]) * inv);
+              w[16 + i] = pack_bf16x2(__uint_as_float(o1[2 * i]) * inv, __uint_as_float(o1[2 * i + 1]) * inv);
+            }
             quad_transpose(w, lane);
+            // now piece s4 of this lane = columns c0 + 16 q .. + 15 of row 4a + s4
 #pragma unroll
             for (int s4 = 0; s4 < 4; ++s4) {
               if (orow[s4] < 0) continue;
-              st_global_v8(p.part_o + orow[s4] + c0, w[8 * s4 + 0], w[8 * s4 + 1], w[8 * s4 + 2], w[8 * s4 + 3],
-                           w[8 * s4 + 4], w[8 * s4 + 5], w[8 * s4 + 6], w[8 * s4 + 7]);
+              __nv_bfloat16* dst = out + orow[s4] + c0;
+              if (wide) {
+                st_global_v8(dst, w[8 * s4 + 0], w[8 * s4 + 1], w[8 * s4 + 2], w[8 * s4 + 3],
+                             w[8 * s4 + 4], w[8 * s4 + 5], w[8 * s4 + 6], w[8 * s4 + 7]);
+              } else {
+                *reinterpret_cast<uint4*>(dst) = make_uint4(w[8 * s4 + 0], w[8 * s4 + 1], w[8 * s4 + 2], w[8 * s4 + 3]);
+                *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[8 * s4 + 4], w[8 * s4 + 5], w[8 * s4 + 6], w[8 * s4 + 7]);
+              }
             }
           }
-          const int tok0 = kTiles * (ud->pair & 0xffff) * TQ;
-          const int tok = tok0 + (both ? t : 0) * TQ + row / G;
-          if (tok < ud->q_len)
-            p.part_ml[partial_row(p, ud->r, ud->pair >> 16, t, both, tok0, tok) * p.a.num_q_heads +
-                      ud->g * G + (row & (G - 1))] = make_float2(m_ref, l);
-        } else {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        // O / l as bf16 in whole 128-byte lines. Each lane holds its own row (TMEM lane =
-        // row); a transpose of 32-byte pieces within each group of four lanes gives lane
-        // 4a + q piece q of rows 4a .. 4a + 3 of the warp, so that one store instruction
-        // writes 8 rows x 128 contiguous bytes instead of 32 rows x 16 bytes (the stores of
-        // one row per lane kept the LSU busy ~4000 cycles per unit).
-        const bool wide = (reinterpret_cast<uintptr_t>(p.a.out) & 31) == 0;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out);
-#pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 64) {
-          uint32_t o0[32], o1[32];
-          tmem_ld32(tO + c0, o0);
-          tmem_ld32(tO + c0 + 32, o1);
-          tmem_wait_ld();
-          uint32_t w[32];  // piece k = words 8k .. 8k + 7 = columns c0 + 16k .. c0 + 16k + 15
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            w[i] = pack_bf16x2(__uint_as_float(o0[2 * i]) * inv, __uint_as_float(o0[2 * i + 1]) * inv);
-            w[16 + i] = pack_bf16x2(__uint_as_float(o1[2 * i]) * inv, __uint_as_float(o1[2 * i + 1]) * inv);
-          }
-          quad_transpose(w, lane);
-          // now piece s4 of this lane = columns c0 + 16 q .. + 15 of row 4a + s4
-#pragma unroll
-          for (int s4 = 0; s4 < 4; ++s4) {
-            if (orow[s4] < 0) continue;
-            __nv_bfloat16* dst = out + orow[s4] + c0;
-            if (wide) {
-              st_global_v8(dst, w[8 * s4 + 0], w[8 * s4 + 1], w[8 * s4 + 2], w[8 * s4 + 3],
-                           w[8 * s4 + 4], w[8 * s4 + 5], w[8 * s4 + 6], w[8 * s4 + 7]);
-            } else {
-              *reinterpret_cast<uint4*>(dst) = make_uint4(w[8 * s4 + 0], w[8 * s4 + 1], w[8 * s4 + 2], w[8 * s4 + 3]);
-              *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[8 * s4 + 4], w[8 * s4 + 5], w[8 * s4 + 6], w[8 * s4 + 7]);
-            }
-          }
-        }
         }
         // O_t is read: the next unit's products may overwrite it
         tcgen05_fence_before();
@@ -1191,8 +1207,8 @@ cudaError_t encode(CUtensorMap* map, void* ptr, int rank, const cuuint64_t* dims
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, bool kShared>
-cudaError_t launch_d(const std::conditional_t<kShared, PrefixArgs, PrefillArgs>& p, cudaStream_t s) {
+template <int D, Pairs kPairs>
+cudaError_t launch_d(const std::conditional_t<kPairs != kWholePairs, PrefixArgs, PrefillArgs>& p, cudaStream_t s) {
   const StepArgs& a = p.a;
   const cuuint64_t e = 2;
   CUtensorMap mk, mv;
@@ -1229,7 +1245,7 @@ cudaError_t launch_d(const std::conditional_t<kShared, PrefixArgs, PrefillArgs>&
     err = encode(&mq, const_cast<void*>(a.q), 3, qd, qs, qb);
     if (err != cudaSuccess) return err;
   }
-  auto kern = prefill_tile_kernel<D, kShared>;
+  auto kern = prefill_tile_kernel<D, kPairs>;
   static DeviceFlags attr_flags;
   std::atomic<bool>& attr_set = device_flag(attr_flags);
   constexpr size_t smem = smem_bytes<D>();
@@ -1244,8 +1260,8 @@ cudaError_t launch_d(const std::conditional_t<kShared, PrefixArgs, PrefillArgs>&
     if (err != cudaSuccess) return err;
     attr_set = true;
   }
-  return launch_pdl(kShared ? kPrefixTc : kPrefillTc, kern, dim3(p.grid), dim3(kThreads), smem, s, mk, mv, mkn, mvn,
-                    mq, p);
+  return launch_pdl(kPairs == kSharedPrefix ? kPrefixTc : kPrefillTc, kern, dim3(p.grid), dim3(kThreads), smem, s, mk, mv,
+                    mkn, mvn, mq, p);
 }
 
 }  // namespace
@@ -1268,22 +1284,28 @@ int prefill_ctas_bound(int num_tokens, int num_requests, int tile_tokens, int nu
 
 cudaError_t prepare_prefill(int head_dim) {
   if (head_dim == 64)
-    return cudaFuncSetAttribute(prefill_tile_kernel<64, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(prefill_tile_kernel<64, kWholePairs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)smem_bytes<64>());
-  return cudaFuncSetAttribute(prefill_tile_kernel<128, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(prefill_tile_kernel<128, kWholePairs>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)smem_bytes<128>());
 }
 
 cudaError_t launch_prefill(const PrefillArgs& p, cudaStream_t stream) {
   if (p.grid <= 0) return cudaSuccess;
-  if (p.a.head_dim == 64) return launch_d<64, false>(p, stream);
-  return launch_d<128, false>(p, stream);
+  if (p.a.head_dim == 64) return launch_d<64, kWholePairs>(p, stream);
+  return launch_d<128, kWholePairs>(p, stream);
 }
 
 cudaError_t launch_prefix(const PrefixArgs& p, cudaStream_t stream) {
   if (p.grid <= 0) return cudaSuccess;
-  if (p.a.head_dim == 64) return launch_d<64, true>(p, stream);
-  return launch_d<128, true>(p, stream);
+  if (p.a.head_dim == 64) return launch_d<64, kSharedPrefix>(p, stream);
+  return launch_d<128, kSharedPrefix>(p, stream);
+}
+
+cudaError_t launch_split_chunks(const PrefixArgs& p, cudaStream_t stream) {
+  if (p.grid <= 0) return cudaSuccess;
+  if (p.a.head_dim == 64) return launch_d<64, kSplitChunks>(p, stream);
+  return launch_d<128, kSplitChunks>(p, stream);
 }
 
 }  // namespace cb

@@ -56,16 +56,20 @@ struct PrefillArgs {
   PrefillEntry entries[kPrefillMaxEntries];  // heaviest first
 };
 
-// The same tiles over a prefix that the requests of a group share: an entry is a group, its
-// "request" r any of the group's (they have the same leading pages), its query tokens the group's
-// packed decode rows, seq_len the prefix's length; every row attends all of it. The key tiles are
-// split into units of tiles_per_unit, whose results are partial rows for the merge. A last query
-// tile without a second one beside it (the tail) is taken by two groups of warps instead, each with
-// one half of every key tile and a partial row of its own. With B the tokens before the
-// tail and R those in it, token i of entry e in split s is row part_row[e] + s B + i (i < B), or
+// The same tiles with the keys of a pair of query tiles split into units of tiles_per_unit key
+// tiles, whose results are partial rows for the merge. Two uses:
+//   launch_prefix: a prefix that a group of decode rows shares. An entry is a group, its "request" r
+//     any of the group's (they have the same leading pages), its query tokens the group's packed
+//     rows, seq_len the prefix's length; every row attends all of it.
+//   launch_split_chunks: chunks, as in PrefillArgs, where there are too few pairs to fill the GPU evenly. A
+//     pair whose keys are one unit is written to the output directly.
+// A last query tile without a second one beside it (the tail) is taken by two groups of warps, each
+// with one half of every key tile and partial rows of its own. With B the tokens before the tail
+// and R those in it, token i of entry e in split s is partial row part_row[e] + s B + i (i < B), or
 // rows tail_row[e] + (2 s + {0, 1}) R + i - B.
 struct PrefixArgs : PrefillArgs {
   int tiles_per_unit;
+  int splits[kPrefillMaxEntries];  // of the entry's longest pair (units past a pair's keys are skipped)
   int part_row[kPrefillMaxEntries];
   int tail_row[kPrefillMaxEntries];
   float* part_o;    // [row][Hq][D] unnormalised
@@ -78,6 +82,7 @@ inline int prefix_splits(int seq_len, int tiles_per_unit) {
   return (prefix_key_tiles(seq_len) + tiles_per_unit - 1) / tiles_per_unit;
 }
 cudaError_t launch_prefix(const PrefixArgs& p, cudaStream_t stream);
+cudaError_t launch_split_chunks(const PrefixArgs& p, cudaStream_t stream);
 
 size_t prefill_smem_bytes(int head_dim);
 // Most prefill CTAs a step of up to `num_tokens` query tokens in `num_requests`

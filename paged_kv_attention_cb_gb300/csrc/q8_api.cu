@@ -49,14 +49,25 @@ Split split_of(int64_t columns, int Hkv) {
 
 int tokens_per_item(const Split& s, int G) { return 8 * s.column_blocks * s.column_warps / G; }
 
+// Units that chunks are split into, at most (a second round of the SMs gains nothing that the first
+// does not have); pieces of a row, at most; and what a unit costs (microseconds of one SM): a
+// 128-key tile against its pair of query tiles, and its start and its rows' way out.
+constexpr int kMaxChunkUnits = 2 * cb::kQ8TableCtas;
+constexpr int kMaxChunkPieces = 64;
+constexpr double kTileUs = 2.0, kUnitUs = 4.0;
+
 // Workspace: header (as cb_paged_attention's), statistics and outputs of the partial rows, then
 // the scratch of the prefilled requests (page table, K pages, V pages), whose sizes follow from
 // each step's lengths.
 struct Layout {
-  size_t part_ml, part_o, scratch;
+  size_t part_ml, part_o;    // of the split kernel
+  size_t chunk_ml, chunk_o;  // of chunks whose keys are split
+  size_t chunk_entries;      // (row, head) partial results there
+  size_t scratch;
 };
 
-Layout layout_of(int64_t R, int64_t T, int Hq, int Hkv, int D) {
+// chunks: whether the step (or the largest one) has requests that are prefilled.
+Layout layout_of(int64_t R, int64_t T, int Hq, int Hkv, int D, bool chunks) {
   const int G = std::max(1, Hq / Hkv);
   int64_t rows = 0;  // (items + CTAs) x warps per head x tokens per item
   for (int columns = std::max(8, G); columns <= 16 * cb::kQ8MaxColumnWarps; columns *= 2) {
@@ -68,7 +79,12 @@ Layout layout_of(int64_t R, int64_t T, int Hq, int Hkv, int D) {
   Layout w;
   w.part_ml = cb::kWorkspaceHeaderBytes;
   w.part_o = w.part_ml + align256((size_t)rows * Hq * 8);
-  w.scratch = w.part_o + align256((size_t)rows * Hq * D * 4);
+  w.chunk_ml = w.part_o + align256((size_t)rows * Hq * D * 4);
+  // a unit has at most 256 (row, head) results
+  w.chunk_entries =
+      chunks ? (size_t)std::min<int64_t>((int64_t)kMaxChunkUnits * 256, T * Hq * kMaxChunkPieces) : 0;
+  w.chunk_o = w.chunk_ml + align256(w.chunk_entries * 8);
+  w.scratch = w.chunk_o + align256(w.chunk_entries * D * 4);
   return w;
 }
 
@@ -95,6 +111,9 @@ struct Q8Plan {
   std::vector<cb::MergeRow> merge;
   int max_pieces = 0;
   std::vector<cb::PrefillEntry> chunks;  // heaviest first
+  int chunk_tiles = 0;                   // key tiles per unit of theirs (0: whole pairs)
+  std::vector<cb::MergeRow> chunk_merge;
+  int chunk_pieces = 0;
 };
 
 int first_key(int pos0, int window) { return window > 0 ? std::max(0, pos0 - window + 1) : 0; }
@@ -241,21 +260,88 @@ size_t plan_chunks(Q8Plan& plan, const cb::StepArgs& a, int max_q, const int32_t
   return scratch_bytes(table, pages, a.block_size, a.num_kv_heads, a.head_dim);
 }
 
-// The prefilled requests, up to kPrefillMaxEntries a launch: their pages as bf16, then the tiles.
-cudaError_t run_chunks(const Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c,
-                       uint8_t* scratch, cudaStream_t s) {
+// Key tiles that a pair of a chunk's query tiles attends.
+int pair_tiles(const cb::PrefillEntry& e, int pair, int TQ, int window) {
+  const int ctx = e.seq_len - e.q_len, tok0 = 2 * pair * TQ, end = std::min(e.q_len, tok0 + 2 * TQ);
+  return (ctx + end - 1) / 128 - first_key(ctx + tok0, window) / 128 + 1;
+}
+
+// Pieces that the keys of an entry's longest pair are split into.
+int entry_splits(const cb::PrefillEntry& e, int TQ, int window, int per) {
+  int splits = 1;
+  for (int p = 0; 2 * p < e.n_qtiles; ++p)
+    splits = std::max(splits, (pair_tiles(e, p, TQ, window) + per - 1) / per);
+  return splits;
+}
+
+// Tokens of an entry before its tail (a last query tile without a second one).
+int body_tokens(const cb::PrefillEntry& e, int TQ) { return e.n_qtiles % 2 ? (e.n_qtiles - 1) * TQ : e.q_len; }
+
+// Partial rows of an entry: every split of the body where there is more than one, twice as many of
+// the tail (its key tiles are halved).
+long long entry_rows(const cb::PrefillEntry& e, int TQ, int splits) {
+  const int body = body_tokens(e, TQ);
+  return (splits > 1 ? (long long)splits * body : 0) + 2LL * splits * (e.q_len - body);
+}
+
+// Whether and how far the chunks' keys are split. Whole pairs take no merge, but leave SMs idle
+// where there are few of them: the longest pair is the time while they are no more than the SMs.
+// Otherwise all units' time over the SMs and half a unit for the uneven end; for a split also the
+// partial rows written and read again (about 4 TB/s) and the merge's launches. The least time is
+// taken, a split only where it gains a tenth.
+void split_chunks(Q8Plan& plan, const cb::StepArgs& a, size_t max_entries) {
+  const int TQ = 128 / (a.num_q_heads / a.num_kv_heads), W = a.sliding_window, S = cb::sm_count();
+  long long pairs = 0, tiles = 0;
+  int longest = 1;
+  for (const cb::PrefillEntry& e : plan.chunks)
+    for (int p = 0; 2 * p < e.n_qtiles; ++p) {
+      const int n = pair_tiles(e, p, TQ, W);
+      longest = std::max(longest, n);
+      tiles += n;
+      ++pairs;
+    }
+  auto time = [&](long long units, int per) {
+    const double unit = per * kTileUs + kUnitUs;
+    if (units * a.num_kv_heads <= S) return unit;
+    return std::max(unit, (tiles * kTileUs + units * kUnitUs) * a.num_kv_heads / S + 0.5 * unit);
+  };
+  double best = 0.9 * time(pairs, longest);
+  for (int k = 2; k <= kMaxChunkPieces / 2 && k <= longest; ++k) {  // pieces of the longest pair
+    const int per = (longest + k - 1) / k;
+    if (pairs * a.num_kv_heads * (k - 1) > kMaxChunkUnits) break;
+    long long units = 0, rows = 0;
+    for (const cb::PrefillEntry& e : plan.chunks) {
+      rows += entry_rows(e, TQ, entry_splits(e, TQ, W, per));
+      for (int p = 0; 2 * p < e.n_qtiles; ++p) units += (pair_tiles(e, p, TQ, W) + per - 1) / per;
+    }
+    const double t = time(units, per) + (double)rows * a.num_q_heads * a.head_dim * 8 / 4e6 +
+                     3.0 * (double)((a.num_tokens + 1023) / 1024);
+    if ((size_t)rows * a.num_q_heads <= max_entries && t < best) {
+      best = t;
+      plan.chunk_tiles = per;
+    }
+  }
+}
+
+// The prefilled requests, up to kPrefillMaxEntries a launch: their pages as bf16, the tiles, and
+// the merge of the rows whose keys were split.
+cudaError_t run_chunks(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, const Layout& w,
+                       uint8_t* ws, cudaStream_t s) {
   int64_t table = 0, total = 0;
   for (const cb::PrefillEntry& e : plan.chunks) {
     const int64_t all = ((int64_t)e.seq_len + a.block_size - 1) / a.block_size;
     table += all;
     total += all - first_key(e.seq_len - e.q_len, a.sliding_window) / 128 * 128 / a.block_size;
   }
+  uint8_t* scratch = ws + w.scratch;
   uint8_t* k = scratch + align256((size_t)table * 4);
   uint8_t* v = k + (size_t)total * a.block_size * a.num_kv_heads * a.head_dim * 2;
-  int row = 0, dst = 0;
+  const int TQ = 128 / (a.num_q_heads / a.num_kv_heads), per = plan.chunk_tiles;
+  int row = 0, dst = 0, part = 0;
+  static thread_local cb::DequantArgs d;
+  static thread_local cb::PrefixArgs pa;
   for (size_t i = 0; i < plan.chunks.size(); i += cb::kPrefillMaxEntries) {
     const int n = (int)std::min<size_t>(cb::kPrefillMaxEntries, plan.chunks.size() - i);
-    cb::DequantArgs d = {};
     d.c = c;
     d.block_table = a.block_table;
     d.bt_stride = a.bt_stride;
@@ -268,48 +354,80 @@ cudaError_t run_chunks(const Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Ca
     d.table = reinterpret_cast<int32_t*>(scratch);
     d.error_word = a.error_word;
     d.dst0 = dst;
-    cb::PrefillArgs pa = {};
+    static_cast<cb::PrefillArgs&>(pa) = cb::PrefillArgs{};
     pa.a = a;
     pa.a.k_cache = k;
     pa.a.v_cache = v;
     pa.a.block_table = d.table;
     pa.a.bt_stride = 1;  // an entry's "request" is the offset of its table row
     pa.a.num_blocks = (int)total;
-    pa.tile_tokens = 128 / (a.num_q_heads / a.num_kv_heads);
+    pa.tile_tokens = TQ;
     pa.box_keys = std::min(a.block_size, 128);
     pa.metadata_ready = 1;
     int* header = a.error_word;  // the workspace's first word
     pa.exit_counter = header + cb::kExitCounterOffset / 4;
     pa.unit_counter = header + cb::kUnitCounterOffset / 4;
     pa.scatter_counter = header + cb::kScatterCounterOffset / 4;
+    pa.tiles_per_unit = per;  // (0: none of these are read)
+    pa.part_ml = reinterpret_cast<float2*>(ws + w.chunk_ml);
+    pa.part_o = reinterpret_cast<float*>(ws + w.chunk_o);
     for (int j = 0; j < n; ++j) {
       cb::PrefillEntry e = plan.chunks[i + j];
       const int all = (e.seq_len + a.block_size - 1) / a.block_size;
       const int first =
           first_key(e.seq_len - e.q_len, a.sliding_window) / 128 * 128 / a.block_size;
       d.entries[j] = cb::DequantEntry{e.r, first, all - first, dst, row};
+      int splits = 1;
+      if (per > 0) {
+        const int body = body_tokens(e, TQ);
+        splits = entry_splits(e, TQ, a.sliding_window, per);
+        const int tail_row = part + (splits > 1 ? splits * body : 0);
+        pa.splits[j] = splits;
+        pa.part_row[j] = part;
+        pa.tail_row[j] = tail_row;
+        for (int p = 0; 2 * p < e.n_qtiles; ++p) {
+          const int ks = (pair_tiles(e, p, TQ, a.sliding_window) + per - 1) / per;
+          const bool tail = 2 * p + 1 == e.n_qtiles;
+          if (ks == 1 && !tail) continue;  // written directly
+          const int pieces = tail ? 2 * ks : ks;
+          for (int t = 2 * p * TQ; t < std::min(e.q_len, 2 * (p + 1) * TQ); ++t)
+            plan.chunk_merge.push_back(
+                tail ? cb::MergeRow{e.q_start + t, tail_row + t - body, e.q_len - body, pieces, 0, 0, 0}
+                     : cb::MergeRow{e.q_start + t, part + t, body, pieces, 0, 0, 0});
+          plan.chunk_pieces = std::max(plan.chunk_pieces, pieces);
+        }
+        part += (int)entry_rows(e, TQ, splits);
+      }
       e.r = row;
       pa.entries[j] = e;
-      pa.total_ctas += cb::prefill_ctas(e.n_qtiles, a.num_kv_heads);
+      pa.total_units += (e.n_qtiles + 1) / 2 * a.num_kv_heads * splits;
       row += all;
       dst += all - first;
     }
     d.n_entries = pa.n_entries = n;
     d.n_pages = dst - d.dst0;
-    pa.total_units = pa.total_ctas;
+    pa.total_ctas = pa.total_units;
     pa.grid = std::min(pa.total_units, cb::sm_count());
     cudaError_t e = cb::launch_dequant_pages_q8(d, s);
-    if (e == cudaSuccess) e = cb::launch_prefill(pa, s);
+    if (e == cudaSuccess) e = per > 0 ? cb::launch_split_chunks(pa, s) : cb::launch_prefill(pa, s);
     if (e != cudaSuccess) return e;
   }
-  return cudaSuccess;
+  if (plan.chunk_merge.empty()) return cudaSuccess;
+  cb::MergeArgs m;
+  m.out = a.out;
+  m.dtype = a.dtype;
+  m.num_q_heads = a.num_q_heads;
+  m.head_dim = a.head_dim;
+  m.part_o = pa.part_o;
+  m.part_ml = pa.part_ml;
+  m.parts = cb::merge_parts(plan.chunk_pieces);
+  return cb::launch_merge(m, plan.chunk_merge.data(), (int)plan.chunk_merge.size(), s);
 }
 
-cb_status check_rows(const char* what, const void* k, const void* v, const cb::Q8Cache& c,
+cb_status check_rows(const void* k, const void* v, const cb::Q8Cache& c,
                      const int64_t* slot_mapping, int32_t num_tokens, int32_t num_blocks,
                      int32_t block_size, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
                      bool* empty) {
-  (void)what;
   *empty = false;
   if (dtype != CB_F32 && dtype != CB_BF16)
     return report_error(CB_ERR_INVALID_ARG, "dtype must be CB_F32 or CB_BF16");
@@ -350,7 +468,7 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
                                       num_kv_heads, head_dim, block_table_stride, dtype,
                                       h_query_start_loc, h_seq_lens);
   if (st != CB_OK) return st;
-  const Layout w = layout_of(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim);
+  Layout w = layout_of(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim, false);
   if (!workspace || workspace_bytes < w.scratch)
     return report_error(CB_ERR_WORKSPACE, "workspace missing or smaller than cb_workspace_size_q8()");
   if (!cb::is_aligned16(workspace))
@@ -403,15 +521,19 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
   plan.split = false;
   plan.merge.clear();
   plan.chunks.clear();
+  plan.chunk_merge.clear();
+  plan.chunk_tiles = plan.chunk_pieces = 0;
   plan.max_pieces = 0;
   if (fast) {
     const int G = num_q_heads / num_kv_heads;
     const int max_q = dtype == CB_F32 ? INT_MAX : std::max(1, kChunkColumns / G);
     const size_t need = plan_chunks(plan, a, max_q, h_query_start_loc, h_seq_lens);
-    if (need > workspace_bytes - w.scratch)
+    if (need > 0) w = layout_of(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim, true);
+    if (w.scratch > workspace_bytes || need > workspace_bytes - w.scratch)
       return report_error(CB_ERR_WORKSPACE,
                           "workspace too small for the step's chunks: chunk_kv_tokens of "
                           "cb_workspace_size_q8() must cover the seq_lens of requests with q_len > 1");
+    if (need > 0) split_chunks(plan, a, w.chunk_entries);
     plan_split(plan, a, c, max_q, h_query_start_loc, h_seq_lens, w, ws);
   }
   cudaError_t e = cudaSuccess;
@@ -440,7 +562,7 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
       m.parts = cb::merge_parts(plan.max_pieces);
       e = cb::launch_merge(m, plan.merge.data(), (int)plan.merge.size(), s);
     }
-    if (e == cudaSuccess && !plan.chunks.empty()) e = run_chunks(plan, a, c, ws + w.scratch, s);
+    if (e == cudaSuccess && !plan.chunks.empty()) e = run_chunks(plan, a, c, w, ws, s);
   }
   if (e != cudaSuccess) return cb::report_cuda_error(e, "8-bit attention launch");
   return CB_OK;
@@ -457,7 +579,7 @@ cb_status cb_write_kv_q8(const void* k_new, const void* v_new, void* k_cache, vo
                          int32_t* error_word, void* stream) {
   const cb::Q8Cache c = cache_of(k_cache, v_cache, k_scale, v_scale);
   bool empty = false;
-  const cb_status st = check_rows("write", k_new, v_new, c, slot_mapping, num_tokens, num_blocks,
+  const cb_status st = check_rows(k_new, v_new, c, slot_mapping, num_tokens, num_blocks,
                                   block_size, num_kv_heads, head_dim, dtype, &empty);
   if (st != CB_OK || empty) return st;
   const cudaError_t e = cb::launch_write_kv_q8(
@@ -473,7 +595,7 @@ cb_status cb_read_kv_q8(const void* k_cache, const void* v_cache, const void* k_
                         int32_t* error_word, void* stream) {
   const cb::Q8Cache c = cache_of(k_cache, v_cache, k_scale, v_scale);
   bool empty = false;
-  const cb_status st = check_rows("read", k_out, v_out, c, slot_mapping, num_tokens, num_blocks,
+  const cb_status st = check_rows(k_out, v_out, c, slot_mapping, num_tokens, num_blocks,
                                   block_size, num_kv_heads, head_dim, dtype, &empty);
   if (st != CB_OK || empty) return st;
   const cudaError_t e = cb::launch_read_kv_q8(
@@ -488,7 +610,8 @@ size_t cb_workspace_size_q8(int32_t num_requests, int32_t num_tokens, int32_t nu
   if (num_requests < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       block_size <= 0)
     return cb::kWorkspaceHeaderBytes;
-  const size_t fixed = layout_of(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim).scratch;
+  const size_t fixed = layout_of(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                 chunk_kv_tokens > 0).scratch;
   if (chunk_kv_tokens <= 0) return fixed;
   // each request's pages are rounded up
   const int64_t pages = chunk_kv_tokens / block_size + std::min<int64_t>(num_requests, chunk_kv_tokens);

@@ -102,6 +102,7 @@ void plan_prefix(SharedPlan& sp, const cb::StepArgs& a, int per, int grid_max, i
     p.entries[e] = cb::PrefillEntry{g.r, 2 * t.pairs + t.tail, g.q_start, g.rows, g.prefix};
     p.part_row[e] = row;
     p.tail_row[e] = row + splits * t.body;
+    p.splits[e] = splits;
     p.total_units += (t.pairs + t.tail) * a.num_kv_heads * splits;
     row += (int)partial_rows(g, a, per);
   }

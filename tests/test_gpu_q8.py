@@ -235,6 +235,25 @@ def test_chunks_and_decodes(Hq, Hkv, D, BS, dtype, W):
     assert cb.read_error_word(st.ws) == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv,D,BS,W,q,ctx", [
+    (8, 2, 128, 16, 0, [200], [5000]),             # three pairs of query tiles and a tail
+    (4, 4, 64, 128, 0, [129, 1, 70], [2900, 800, 6001]),
+    (16, 1, 64, 32, 0, [30, 5], [7000, 12000]),    # two full tiles; a tail of five tokens
+    (8, 2, 128, 16, 1500, [257], [9000]),
+    (8, 2, 128, 256, 0, [512, 65], [0, 4000]),     # pairs of one and of many units
+])
+def test_few_chunks_behind_long_contexts(Hq, Hkv, D, BS, W, q, ctx):
+    """The keys of too few query tiles to fill the GPU are split; the pieces are merged."""
+    st = Q8Step(spec_of(q, ctx, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D, block_size=BS,
+                        sliding_window=W, seed=6), seed=3)
+    i = cb.kernel_names().index("merge_rows")
+    before = cb.launch_count(i)
+    st.check(st.run())
+    st.check_cache()
+    assert cb.launch_count(i) > before
+    assert cb.read_error_word(st.ws) == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("Hq,Hkv,D,BS", [(8, 2, 128, 1), (4, 4, 64, 8), (16, 1, 64, 2)])
 def test_small_pages_run_on_the_portable_kernel(Hq, Hkv, D, BS, dtype):
