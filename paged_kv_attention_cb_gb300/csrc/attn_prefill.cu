@@ -103,7 +103,7 @@ struct UnitDesc {
 // tiles' key ranges is walked in key tiles kt0 .. kt0 + nkt - 1.
 struct Geo {
   int r, g, q_start, q_len, seq, ctx, qt0, has_b, tok0, tok_end, kt0, nkt;
-  bool split_all;  // split units: the pair's keys are this one unit
+  bool undivided;  // split units: the pair's keys are this one unit
 };
 
 CB_DEV Geo geo_of(int r, int q_start, int q_len, int seq_len, int g, int pair, int TQ, int W) {
@@ -217,7 +217,7 @@ CB_DEV Geo split_geo(const PrefixArgs& p, const UnitDesc& d, int TQ, int W) {
     e.nkt = (d.seq_len + kKeys - 1) / kKeys;
   }
   const int first = (d.pair >> 16) * p.tiles_per_unit;
-  e.split_all = first == 0 && e.nkt <= p.tiles_per_unit;
+  e.undivided = first == 0 && e.nkt <= p.tiles_per_unit;
   e.kt0 += first;
   e.nkt = min(p.tiles_per_unit, e.nkt - first);
   return e;
@@ -245,13 +245,9 @@ CB_DEV void quad_transpose(uint32_t (&w)[32], int lane) {
   }
 }
 
-// Partial row of token `tok` of entry e in a split (t: the group, tok0: the unit's first token;
-// both: a unit of two query tiles).
-CB_DEV long long partial_row(const PrefixArgs& p, int e, int split, int t, bool both, int tok0, int tok) {
-  const int tiles = p.entries[e].n_qtiles, n = p.entries[e].q_len;
-  const int body = tiles & 1 ? (tiles - 1) * p.tile_tokens : n;  // tokens before the tail
-  if (both) return (long long)p.part_row[e] + (long long)split * body + tok;
-  return (long long)p.tail_row[e] + (long long)(2 * split + t) * (n - body) + (tok - tok0);
+// Partial row of token `tok` of entry e in a split.
+CB_DEV long long partial_row(const PrefixArgs& p, int e, int split, int tok) {
+  return (long long)p.part_row[e] + (long long)split * p.entries[e].q_len + tok;
 }
 
 // The pages of key tile `key_base` in `gen` (bit i: page i of the tile), row by row into
@@ -710,43 +706,20 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
       return mbar_wait_warp_or_abort(&bar.full[i % kStages], (uint32_t)((i / kStages) & 1),
                                      &bar.abort);
     };
-    // Over a shared prefix a unit of one query tile is taken by both groups, each with one half of
-    // every key tile, so that one group's softmax runs beside the other's products as with two
-    // query tiles (one group alone took 1.85 us a key tile, two with a tile each 2.05 us).
-    bool halves = false;
-    constexpr uint32_t idS64 = umma_idesc_bf16(kRows, kKeys / 2, false);
     // S_t = Q_t K^T with K in ring slot i; its completion is signalled on s_full[t]
     auto qk = [&](int t, int i) {
-      uint64_t dq = dQ + (uint64_t)(t * (kTile >> 4));
-      uint64_t dk = dK + (uint64_t)((i % kStages) * (kTile >> 4));
-      uint32_t id = idS;
-      if constexpr (kSplit) {
-        if (halves) {
-          dq = dQ;
-          dk += (uint64_t)(t * ((kKeys / 2 * 128) >> 4));
-          id = idS64;
-        }
-      }
+      const uint64_t dq = dQ + (uint64_t)(t * (kTile >> 4));
+      const uint64_t dk = dK + (uint64_t)((i % kStages) * (kTile >> 4));
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t off = ((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4;
-        umma_bf16_elect(tmem + t * kKeys, dq + off, dk + off, id, ks > 0 ? 1u : 0u);
+        umma_bf16_elect(tmem + t * kKeys, dq + off, dk + off, idS, ks > 0 ? 1u : 0u);
       }
       umma_commit_elect(&bar.s_full[t]);
     };
-    // O_t += P_t V with P in the first columns of S_t and V in ring slot i
+    // O_t += P_t V with P in the first 64 columns of S_t and V in ring slot i
     auto pv = [&](int t, int i, bool acc) {
       const uint64_t dv = dV + (uint64_t)((i % kStages) * (kTile >> 4));
-      if constexpr (kSplit) {
-        if (halves) {
-#pragma unroll
-          for (int ks = 0; ks < kKeys / 32; ++ks)
-            umma_bf16_tmem_a_elect(tmem + 2 * kKeys + t * D, tmem + t * kKeys + ks * 8,
-                                   dv + (uint64_t)((t * (kKeys / 32) + ks) * (2048 >> 4)), idO,
-                                   (acc || ks > 0) ? 1u : 0u);
-          return;
-        }
-      }
 #pragma unroll
       for (int ks = 0; ks < kKeys / 16; ++ks)
         umma_bf16_tmem_a_elect(tmem + 2 * kKeys + t * D, tmem + t * kKeys + ks * 8,
@@ -764,8 +737,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
       if (!d.live) break;
       const Geo e = unit_geo(d);
       const int nkt = e.nkt;
-      if constexpr (kSplit) halves = !e.has_b;
-      const bool has_b = e.has_b || halves;  // group B has work
+      const bool has_b = e.has_b;
       ok = mbar_wait_warp_or_abort(&bar.q_full, (uint32_t)(u & 1), &bar.abort) && slot_ready(i_base);
       if (!ok) break;
       tcgen05_fence_after();
@@ -860,12 +832,10 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         break;
       }
       int kt0, nkt, seq, min_kv, max_kv, tile_max_kv_min, tile_min_kv_max;
-      bool both = true;  // the unit has two query tiles (else, over a shared prefix: this group has
-                         // one half of every key tile)
       {
         const Geo e = CB_UNIT_GEO();
         const int unit_nkt = e.nkt;
-        const bool tile_live = t == 0 || e.has_b || kSplit;
+        const bool tile_live = t == 0 || e.has_b;
         if (!tile_live) {  // this unit has no tile B
           i_base += 2 * unit_nkt;
           CB_RELEASE_UNIT();
@@ -874,8 +844,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         kt0 = e.kt0;
         nkt = e.nkt;
         seq = e.seq;
-        if constexpr (kSplit) both = e.has_b;
-        const int tok0 = (e.qt0 + (kSplit && !e.has_b ? 0 : t)) * TQ;
+        const int tok0 = (e.qt0 + t) * TQ;
         const int qpos = e.ctx + tok0 + row / G;
         max_kv = min(qpos, e.seq - 1);
         min_kv = W > 0 ? max(0, qpos - W + 1) : 0;
@@ -891,26 +860,24 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
       // test hook: the group's first wait runs out (nothing arrives at bar.never)
       if (u == 0 && p.a.test_expire_wait && !mbar_wait_warp_polls(&bar.never, 0, kTestExpiryPolls))
         ok = false;
-      // key tile j of the unit, or this group's half of it (NK keys from `off` on)
-      auto key_tile = [&](auto nk, int j, int off) {
-        constexpr int NK = decltype(nk)::value;
+      for (int j = 0; j < nkt && ok; ++j) {
         if (!mbar_wait_warp_or_abort(&bar.s_full[t], (uint32_t)(swaits++ & 1), &bar.abort)) {
           ok = false;
-          return;
+          break;
         }
         tcgen05_fence_after();
-        uint32_t sr[NK];
+        uint32_t sr[kKeys];
 #pragma unroll
-        for (int c0 = 0; c0 < NK; c0 += 32)
+        for (int c0 = 0; c0 < kKeys; c0 += 32)
           tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(sr + c0));
         tmem_wait_ld();
         float* sv = reinterpret_cast<float*>(sr);
         // mask (bounds only; tiles inside every row's range need none) and row
         // maximum of the raw scores (the scale is positive, so it commutes with max)
-        const int key_base = (kt0 + j) * kKeys + off;
-        if (key_base < tile_min_kv_max || key_base + NK - 1 > tile_max_kv_min) {
+        const int key_base = (kt0 + j) * kKeys;
+        if (key_base < tile_min_kv_max || key_base + kKeys - 1 > tile_max_kv_min) {
 #pragma unroll
-          for (int c = 0; c < NK; ++c) {
+          for (int c = 0; c < kKeys; ++c) {
             const int key = key_base + c;
             if (key < min_kv || key > max_kv) sv[c] = -INFINITY;
           }
@@ -919,7 +886,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
         for (int k = 0; k < 8; ++k) mx8[k] = fmax3(sv[k], sv[8 + 2 * k], sv[9 + 2 * k]);
 #pragma unroll
-        for (int c = 24; c < NK; c += 2) mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], sv[c], sv[c + 1]);
+        for (int c = 24; c < kKeys; c += 2) mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], sv[c], sv[c + 1]);
         const float mx = fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]),
                                fmaxf(mx8[6], mx8[7])) * sl2;
         const bool need = mx > m_ref + kRescaleLog2;
@@ -932,7 +899,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
         for (int k = 0; k < 8; ++k) sum8[k] = 0.f;
 #pragma unroll
-        for (int c = 0; c < NK; c += 2) {
+        for (int c = 0; c < kKeys; c += 2) {
           float x0, x1;
           ffma2(x0, x1, sv[c], sv[c + 1], sl2, -m_ref);
           sv[c] = ex2_approx(x0);
@@ -944,7 +911,7 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         l = l * alpha + sum;
         // P row as bf16 pairs over the first 64 columns of S_t (lane = row)
 #pragma unroll
-        for (int c0 = 0; c0 < NK; c0 += 32) {
+        for (int c0 = 0; c0 < kKeys; c0 += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(sv[c0 + 2 * i], sv[c0 + 2 * i + 1]);
@@ -968,14 +935,14 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         // that 0 * V cannot produce a NaN (row index = key index in the tile).
         // Each group does it before its own P is signalled (the other group may
         // write the same zeros at the same time), so before either PV reads V.
-        if (key_base - off + kKeys > seq) {
+        if (key_base + kKeys > seq) {
           const int iv = i_base - 2 * (nkt - j) + 1;  // V_j of this unit
           if (!mbar_wait_warp_or_abort(&bar.full[iv % kStages], (uint32_t)((iv / kStages) & 1),
                                        &bar.abort)) {
             ok = false;
-            return;
+            break;
           }
-          if (key_base - off + row >= seq) {
+          if (key_base + row >= seq) {
 #pragma unroll
             for (int h = 0; h < kHalves; ++h)
 #pragma unroll
@@ -989,13 +956,6 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
         tcgen05_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar.p_full[t]);
-      };
-      if (kSplit && !both) {
-        if constexpr (kSplit)
-          for (int j = 0; j < nkt && ok; ++j)
-            key_tile(std::integral_constant<int, kKeys / 2>{}, j, t * (kKeys / 2));
-      } else {
-        for (int j = 0; j < nkt && ok; ++j) key_tile(std::integral_constant<int, kKeys>{}, j, 0);
       }
       // ---- epilogue: O / l for the rows of this tile. The rows' output offsets are
       // computed while the last PV product runs (~600 cycles after the wait otherwise).
@@ -1004,15 +964,15 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
       long long orow[4];  // output offset of rows 4a .. 4a + 3 of the warp, -1 past q_len
       {
         const Geo e = CB_UNIT_GEO();
-        if constexpr (kPairs == kSplitChunks) partial = !(both && e.split_all);
+        if constexpr (kPairs == kSplitChunks) partial = !e.undivided;
         const int lg = __ffs(G) - 1;
 #pragma unroll
         for (int s4 = 0; s4 < 4; ++s4) {
           const int r = (warp & 3) * 32 + 4 * (lane >> 2) + s4;  // tile row
-          const int tok = (e.qt0 + (kSplit && !both ? 0 : t)) * TQ + (r >> lg);
+          const int tok = (e.qt0 + t) * TQ + (r >> lg);
           if (partial) {  // offset in the partial rows, four fp32 pieces a line
             if constexpr (kSplit) {
-              const long long pr = partial_row(p, ud->r, ud->pair >> 16, t, both, e.tok0, tok);
+              const long long pr = partial_row(p, ud->r, ud->pair >> 16, tok);
               orow[s4] = tok < e.q_len ? (pr * p.a.num_q_heads + e.g * G + (r & (G - 1))) * D + q4 * 8 : -1;
             }
           } else {
@@ -1055,11 +1015,9 @@ prefill_tile_kernel(const __grid_constant__ CUtensorMap tmap_k,
                              w[8 * s4 + 4], w[8 * s4 + 5], w[8 * s4 + 6], w[8 * s4 + 7]);
               }
             }
-            const int tok0 = kTiles * (ud->pair & 0xffff) * TQ;
-            const int tok = tok0 + (both ? t : 0) * TQ + row / G;
+            const int tok = (kTiles * (ud->pair & 0xffff) + t) * TQ + row / G;
             if (tok < ud->q_len)
-              p.part_ml[partial_row(p, ud->r, ud->pair >> 16, t, both, tok0, tok) * p.a.num_q_heads +
-                        ud->g * G + (row & (G - 1))] = make_float2(m_ref, l);
+              p.part_ml[partial_row(p, ud->r, ud->pair >> 16, tok) * p.a.num_q_heads + ud->g * G + (row & (G - 1))] = make_float2(m_ref, l);
           }
         }
         if (!partial) {

@@ -63,15 +63,11 @@ struct PrefillArgs {
 //     rows, seq_len the prefix's length; every row attends all of it.
 //   launch_split_chunks: chunks, as in PrefillArgs, where there are too few pairs to fill the GPU evenly. A
 //     pair whose keys are one unit is written to the output directly.
-// A last query tile without a second one beside it (the tail) is taken by two groups of warps, each
-// with one half of every key tile and partial rows of its own. With B the tokens before the tail
-// and R those in it, token i of entry e in split s is partial row part_row[e] + s B + i (i < B), or
-// rows tail_row[e] + (2 s + {0, 1}) R + i - B.
+// Token i of entry e in split s is partial row part_row[e] + s q_len + i.
 struct PrefixArgs : PrefillArgs {
   int tiles_per_unit;
   int splits[kPrefillMaxEntries];  // of the entry's longest pair (units past a pair's keys are skipped)
   int part_row[kPrefillMaxEntries];
-  int tail_row[kPrefillMaxEntries];
   float* part_o;    // [row][Hq][D] unnormalised
   float2* part_ml;  // [row][Hq] (running maximum in log2 units, sum)
 };

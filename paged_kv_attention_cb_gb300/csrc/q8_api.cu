@@ -54,7 +54,7 @@ int tokens_per_item(const Split& s, int G) { return 8 * s.column_blocks * s.colu
 // 128-key tile against its pair of query tiles, and its start and its rows' way out.
 constexpr int kMaxChunkUnits = 2 * cb::kQ8TableCtas;
 constexpr int kMaxChunkPieces = 64;
-constexpr double kTileUs = 2.0, kUnitUs = 4.0;
+constexpr double kTileUs = 1.9, kUnitUs = 4.0;
 
 // Workspace: header (as cb_paged_attention's), statistics and outputs of the partial rows, then
 // the scratch of the prefilled requests (page table, K pages, V pages), whose sizes follow from
@@ -274,16 +274,6 @@ int entry_splits(const cb::PrefillEntry& e, int TQ, int window, int per) {
   return splits;
 }
 
-// Tokens of an entry before its tail (a last query tile without a second one).
-int body_tokens(const cb::PrefillEntry& e, int TQ) { return e.n_qtiles % 2 ? (e.n_qtiles - 1) * TQ : e.q_len; }
-
-// Partial rows of an entry: every split of the body where there is more than one, twice as many of
-// the tail (its key tiles are halved).
-long long entry_rows(const cb::PrefillEntry& e, int TQ, int splits) {
-  const int body = body_tokens(e, TQ);
-  return (splits > 1 ? (long long)splits * body : 0) + 2LL * splits * (e.q_len - body);
-}
-
 // Whether and how far the chunks' keys are split. Whole pairs take no merge, but leave SMs idle
 // where there are few of them: the longest pair is the time while they are no more than the SMs.
 // Otherwise all units' time over the SMs and half a unit for the uneven end; for a split also the
@@ -306,12 +296,13 @@ void split_chunks(Q8Plan& plan, const cb::StepArgs& a, size_t max_entries) {
     return std::max(unit, (tiles * kTileUs + units * kUnitUs) * a.num_kv_heads / S + 0.5 * unit);
   };
   double best = 0.9 * time(pairs, longest);
-  for (int k = 2; k <= kMaxChunkPieces / 2 && k <= longest; ++k) {  // pieces of the longest pair
+  for (int k = 2; k <= kMaxChunkPieces && k <= longest; ++k) {  // pieces of the longest pair
     const int per = (longest + k - 1) / k;
     if (pairs * a.num_kv_heads * (k - 1) > kMaxChunkUnits) break;
     long long units = 0, rows = 0;
     for (const cb::PrefillEntry& e : plan.chunks) {
-      rows += entry_rows(e, TQ, entry_splits(e, TQ, W, per));
+      const int splits = entry_splits(e, TQ, W, per);
+      if (splits > 1) rows += (long long)splits * e.q_len;
       for (int p = 0; 2 * p < e.n_qtiles; ++p) units += (pair_tiles(e, p, TQ, W) + per - 1) / per;
     }
     const double t = time(units, per) + (double)rows * a.num_q_heads * a.head_dim * 8 / 4e6 +
@@ -379,24 +370,17 @@ cudaError_t run_chunks(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c
       d.entries[j] = cb::DequantEntry{e.r, first, all - first, dst, row};
       int splits = 1;
       if (per > 0) {
-        const int body = body_tokens(e, TQ);
         splits = entry_splits(e, TQ, a.sliding_window, per);
-        const int tail_row = part + (splits > 1 ? splits * body : 0);
         pa.splits[j] = splits;
         pa.part_row[j] = part;
-        pa.tail_row[j] = tail_row;
         for (int p = 0; 2 * p < e.n_qtiles; ++p) {
-          const int ks = (pair_tiles(e, p, TQ, a.sliding_window) + per - 1) / per;
-          const bool tail = 2 * p + 1 == e.n_qtiles;
-          if (ks == 1 && !tail) continue;  // written directly
-          const int pieces = tail ? 2 * ks : ks;
+          const int pieces = (pair_tiles(e, p, TQ, a.sliding_window) + per - 1) / per;
+          if (pieces == 1) continue;  // written directly
           for (int t = 2 * p * TQ; t < std::min(e.q_len, 2 * (p + 1) * TQ); ++t)
-            plan.chunk_merge.push_back(
-                tail ? cb::MergeRow{e.q_start + t, tail_row + t - body, e.q_len - body, pieces, 0, 0, 0}
-                     : cb::MergeRow{e.q_start + t, part + t, body, pieces, 0, 0, 0});
+            plan.chunk_merge.push_back(cb::MergeRow{e.q_start + t, part + t, e.q_len, pieces, 0, 0, 0});
           plan.chunk_pieces = std::max(plan.chunk_pieces, pieces);
         }
-        part += (int)entry_rows(e, TQ, splits);
+        if (splits > 1) part += splits * e.q_len;
       }
       e.r = row;
       pa.entries[j] = e;

@@ -2,7 +2,7 @@
 // leading pages are the same. With P the prefix of request r's group,
 //     out = sum_{p < P} 2^s_p v_p + sum_{P <= p} 2^s_p v_p, over the sum of the weights:
 // the first part for all rows of a group at once, as dense tiles of 128 rows on the tensor cores
-// that read the prefix's K/V once per 256 rows (prefill_tile_kernel with kShared), the second
+// that read the prefix's K/V once per 256 rows (prefill_tile_kernel's kSharedPrefix), the second
 // row by row from each request's own pages (decode_split_kernel from position P on), joined by
 // log-sum-exp (merge.h).
 //
@@ -40,10 +40,13 @@ size_t shared_bytes(int64_t R, int64_t T, int64_t Hq, int64_t D) {
   return cb::kWorkspaceHeaderBytes + align256(n * 8) + n * D * 4;
 }
 
-// Measured on GB300 (32 and 16 rows of 8 heads, prefixes of 32768 and 131072): microseconds of one
-// SM for a 128-key tile against two query tiles (tensor pipe and softmax) and, in a tail, against
-// one (the keys' bytes: 5.3 TB/s over all SMs); and for a unit's start and its partial rows.
-constexpr double kPairUs = 2.05, kTailUs = 1.85, kUnitUs = 4.0;
+// Measured on GB300 (32 and 16 rows of 64 query heads behind 131072 positions of 8 KV heads: 106.4
+// and 95.5 us): microseconds of one SM for a 128-key tile against two query tiles (tensor pipe and
+// softmax) and, in a tail, against one (the keys' bytes: 5.6 TB/s over all SMs); and for a unit's
+// start and its partial rows. A tail taken by both softmax groups with one half of each key tile was
+// slower than by one of them: 99.0 us there, and with a pair beside it (37 rows in each of four
+// groups, 32768 positions) 246 instead of 209 us.
+constexpr double kPairUs = 1.9, kTailUs = 1.7, kUnitUs = 4.0;
 constexpr double kHbm = 6.6e12;
 
 // The plain step, which reads the shared pages from L2 after the first request: a start of 9 us
@@ -67,20 +70,17 @@ struct SharedPlan {
 
 int rows_per_tile(const cb::StepArgs& a) { return 128 / (a.num_q_heads / a.num_kv_heads); }
 
-// A group's query tiles: pairs of them, a tail or none, and the tokens before the tail.
+// A group's query tiles: pairs of them, and a last one without a second (tail) or not.
 struct Tiles {
-  int pairs, tail, body;
+  int pairs, tail;
 };
 
 Tiles tiles_of(const Group& g, const cb::StepArgs& a) {
   const int tq = rows_per_tile(a), tiles = (g.rows + tq - 1) / tq;
-  return Tiles{tiles / 2, tiles % 2, tiles % 2 ? (tiles - 1) * tq : g.rows};
+  return Tiles{tiles / 2, tiles % 2};
 }
 
-int64_t partial_rows(const Group& g, const cb::StepArgs& a, int per) {
-  const Tiles t = tiles_of(g, a);
-  return (int64_t)cb::prefix_splits(g.prefix, per) * (t.body + 2 * (g.rows - t.body));
-}
+int64_t partial_rows(const Group& g, int per) { return (int64_t)cb::prefix_splits(g.prefix, per) * g.rows; }
 
 void plan_prefix(SharedPlan& sp, const cb::StepArgs& a, int per, int grid_max, int first_row) {
   cb::PrefixArgs& p = sp.prefix;
@@ -101,10 +101,9 @@ void plan_prefix(SharedPlan& sp, const cb::StepArgs& a, int per, int grid_max, i
     const int e = p.n_entries++, splits = cb::prefix_splits(g.prefix, per);
     p.entries[e] = cb::PrefillEntry{g.r, 2 * t.pairs + t.tail, g.q_start, g.rows, g.prefix};
     p.part_row[e] = row;
-    p.tail_row[e] = row + splits * t.body;
     p.splits[e] = splits;
     p.total_units += (t.pairs + t.tail) * a.num_kv_heads * splits;
-    row += (int)partial_rows(g, a, per);
+    row += (int)partial_rows(g, per);
   }
   p.total_ctas = p.total_units;
   p.grid = std::min(p.total_units, grid_max);
@@ -168,7 +167,7 @@ Choice choose(const SharedPlan& sp, const cb::StepArgs& a, double decode_bytes, 
     for (const Group& g : sp.groups) {
       const Tiles t = tiles_of(g, a);
       units += (long long)(t.pairs + t.tail) * a.num_kv_heads * cb::prefix_splits(g.prefix, per);
-      rows += partial_rows(g, a, per);
+      rows += partial_rows(g, per);
     }
     if ((size_t)rows <= max_rows) {
       const double us = per * mean_us + kUnitUs;
@@ -237,7 +236,7 @@ bool plan_shared(SharedPlan& sp, const cb::StepArgs& a, const int32_t* qsl, cons
   const int C = std::max(1, (plan.concurrent ? S - ch.k : S) / hg);
   const long long slots = a.num_requests + C;
   size_t rows = 0;
-  for (const Group& g : sp.groups) rows += (size_t)partial_rows(g, a, per);
+  for (const Group& g : sp.groups) rows += (size_t)partial_rows(g, per);
   if ((slots + rows) * a.num_q_heads > entries) return false;
   cb::plan_decode(plan, a, qsl, seq, prefix, U, C, scatter);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -259,11 +258,9 @@ bool plan_shared(SharedPlan& sp, const cb::StepArgs& a, const int32_t* qsl, cons
     cb::MergeRow m{qsl[r], r + b0, 1, b1 - b0 + 1, 0, 0, 0};
     if (sp.group_of[r] >= 0) {
       const Group& g = sp.groups[sp.group_of[r]];
-      const int e = sp.group_of[r], i = qsl[r] - g.q_start, body = tiles_of(g, a).body;
-      const bool tail = i >= body;
-      m.b = tail ? sp.prefix.tail_row[e] + i - body : sp.prefix.part_row[e] + i;
-      m.b_step = tail ? g.rows - body : body;
-      m.nb = cb::prefix_splits(g.prefix, per) * (tail ? 2 : 1);
+      m.b = sp.prefix.part_row[sp.group_of[r]] + qsl[r] - g.q_start;
+      m.b_step = g.rows;
+      m.nb = cb::prefix_splits(g.prefix, per);
     } else if (b1 == b0) {
       continue;
     }
