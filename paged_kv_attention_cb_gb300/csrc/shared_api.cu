@@ -55,6 +55,10 @@ constexpr double kHbm = 6.6e12;
 // (16 requests behind 2048 positions: 14.7 us shared, 20.7 plain; behind 512: 14.2 and 12.6).
 constexpr double kPlainUs = 9.0, kPlainBlockUs = 0.82, kSharedUs = 9.5;
 
+// A decode row's share of the decode grid's time besides its key blocks: its query, first maximum
+// and partial rows (148 rows of up to 700 own positions on 12 SMs: 256 us, on 40: 87 us).
+constexpr double kDecodeRowUs = 3.0;
+
 struct Group {
   int r, q_start, rows, prefix;
 };
@@ -136,7 +140,8 @@ struct Choice {
 // The SM share and the split of the key tiles with the least modelled time: the decode stream on
 // its SMs, the prefix's units on the others and then on all, and the merge of the partial rows
 // (written and read once at L2's rate).
-Choice choose(const SharedPlan& sp, const cb::StepArgs& a, double decode_bytes, double decode_blocks,
+// decode_us: the decode's time on one SM.
+Choice choose(const SharedPlan& sp, const cb::StepArgs& a, double decode_bytes, double decode_us,
               int S, bool beside, size_t max_rows) {
   int longest = 0;
   double tile_us = 0.0;  // of all key tiles
@@ -172,8 +177,7 @@ Choice choose(const SharedPlan& sp, const cb::StepArgs& a, double decode_bytes, 
     if ((size_t)rows <= max_rows) {
       const double us = per * mean_us + kUnitUs;
       for (int k = 4; k < S; k += k < 28 ? 8 : 14) {
-        const double td = std::max(decode_bytes / kHbm * 1e6,
-                                   decode_blocks * kPlainBlockUs / (beside ? S - k : S));
+        const double td = std::max(decode_bytes / kHbm * 1e6, decode_us / (beside ? S - k : S));
         const double merge = (double)rows * row_us;
         if (std::max(td, (double)units * us / S) + merge >= best.us * 0.97) continue;  // cannot be better
         const double tp = beside ? done_at(units, us, k, S - k, td) : td + done_at(units, us, S, 0, 0.0);
@@ -217,18 +221,20 @@ bool plan_shared(SharedPlan& sp, const cb::StepArgs& a, const int32_t* qsl, cons
   plan.concurrent = plan.n_prefill_launches == 0;
   plan.fused_scatter = scatter != nullptr && plan.concurrent;
 
-  long long U = 0, U_plain = 0;
+  long long U = 0, U_plain = 0, decode_rows = 0;
   for (int r = 0; r < a.num_requests; ++r) {
     if (qsl[r + 1] - qsl[r] != 1) continue;
     U += cb::decode_units_host(seq[r], 0, prefix[r]);
     U_plain += cb::decode_units_host(seq[r], 0, 0);
+    ++decode_rows;
   }
   const int S = std::min(cb::sm_count(), kMaxDecodeCtasShared);
   const int hg = a.num_kv_heads / plan.decode.heads_per_cta;
   const size_t entries = partial_entries(a.num_requests, a.num_tokens, a.num_q_heads);
   const size_t slots_max = (size_t)a.num_requests + S;
   const double bytes = (double)U * 16 * 2 * a.num_kv_heads * a.head_dim * 2;
-  const Choice ch = choose(sp, a, bytes, (double)U * hg, S, plan.concurrent, entries / a.num_q_heads - slots_max);
+  const Choice ch = choose(sp, a, bytes, hg * (U * kPlainBlockUs + decode_rows * kDecodeRowUs), S, plan.concurrent,
+                           entries / a.num_q_heads - slots_max);
   const int per = ch.per;
   const double plain_us = kPlainUs + kPlainBlockUs * (double)U_plain * hg / S;
   if (ch.us + kSharedUs >= plain_us && !(flags & CB_FLAG_SHARE_ALWAYS)) return false;
