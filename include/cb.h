@@ -404,7 +404,8 @@ cb_status cb_read_kv_q8(const void* k_cache, const void* v_cache, const void* k_
  * with q_len > 1 of one step have together; 0 for steps of decode rows only (and for fp32
  * steps, which need no scratch for them). Long query runs (more than 64 query columns, tokens
  * times the group size) are computed from a bf16 copy of their requests' pages, which lives
- * there for the step: 4 Hkv D bytes a position.
+ * there for the step: 4 Hkv D bytes a position, beside partial results of up to 400 (Hq D)
+ * rows a token or 50 MB.
  * The workspace is initialised with cb_workspace_init and its error word read with
  * cb_read_error_word, as cb_paged_attention's.
  */
@@ -424,7 +425,10 @@ size_t cb_workspace_size_q8(int32_t num_requests, int32_t num_tokens, int32_t nu
  * of q, out, k_new and v_new; CB_FLAG_PORTABLE_ONLY is honoured), with the two scale arrays
  * after the caches. Scale bytes of attended rows lie in 1 .. 254.
  *
- * Block sizes that are multiples of 16 run on the tensor cores; smaller ones on the CUDA cores.
+ * Block sizes that are multiples of 16 run on the tensor cores; smaller ones, and more than 128
+ * KV heads, on the CUDA cores. Cache rows that no token of a request attends may hold anything. In
+ * long query runs (as above) a NaN in a V row that some tokens of the run attend may reach the
+ * others of the run too.
  * CB_ERR_WORKSPACE where the workspace is smaller than cb_workspace_size_q8() says for the
  * step's sizes, chunk_kv_tokens included. Calls that share a workspace are ordered on one
  * stream; so a captured call and its replays keep the workspace to themselves.

@@ -166,7 +166,9 @@ read_kv_q8_kernel(T* __restrict__ k_out, T* __restrict__ v_out, Q8Cache c,
   store16(v_out + row * D + part * kVals, x);
 }
 
-// One CTA per destination page. A page id out of range reads as zeros.
+// One CTA per destination page. A page id out of range reads as zeros, and so do positions that
+// no row attends (before a sliding window: they may hold anything, and the tiles multiply them by
+// weights of zero). A thread has the loads of up to four pieces of both rows in flight.
 template <int D>
 __global__ void __launch_bounds__(kThreads) dequant_pages_q8_kernel(const __grid_constant__ DequantArgs d) {
   constexpr int LPR = D / kVals;
@@ -190,21 +192,33 @@ __global__ void __launch_bounds__(kThreads) dequant_pages_q8_kernel(const __grid
   const int64_t from = (int64_t)(ok ? src : 0) * rows, to = (int64_t)page * rows;
   __nv_bfloat16* ko = static_cast<__nv_bfloat16*>(d.k) + to * D;
   __nv_bfloat16* vo = static_cast<__nv_bfloat16*>(d.v) + to * D;
-  for (int i = threadIdx.x; i < rows * LPR; i += kThreads) {
-    const int row = i / LPR;
-    uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
-    float sk = 0.f, sv = 0.f;
-    if (ok) {
-      k = __ldg(reinterpret_cast<const uint4*>(d.c.k + from * D) + i);
-      v = __ldg(reinterpret_cast<const uint4*>(d.c.v + from * D) + i);
-      sk = e8m0_value(__ldg(d.c.k_scale + from + row));
-      sv = e8m0_value(__ldg(d.c.v_scale + from + row));
+  const int unread = max(0, e.first_pos - lp * d.block_size) * d.num_kv_heads;  // leading rows
+  constexpr int kBatch = 4;
+  for (int i0 = threadIdx.x; i0 < rows * LPR; i0 += kThreads * kBatch) {
+    uint4 k[kBatch], v[kBatch];
+    float sk[kBatch], sv[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * kThreads, row = i / LPR;
+      k[b] = v[b] = make_uint4(0u, 0u, 0u, 0u);
+      sk[b] = sv[b] = 0.f;
+      if (ok && i < rows * LPR && row >= unread) {
+        k[b] = __ldg(reinterpret_cast<const uint4*>(d.c.k + from * D) + i);
+        v[b] = __ldg(reinterpret_cast<const uint4*>(d.c.v + from * D) + i);
+        sk[b] = e8m0_value(__ldg(d.c.k_scale + from + row));
+        sv[b] = e8m0_value(__ldg(d.c.v_scale + from + row));
+      }
     }
-    float x[kVals];
-    dequant16(k, sk, x);
-    store16(ko + i * kVals, x);
-    dequant16(v, sv, x);
-    store16(vo + i * kVals, x);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int i = i0 + b * kThreads;
+      if (i >= rows * LPR) break;
+      float x[kVals];
+      dequant16(k[b], sk[b], x);
+      store16(ko + i * kVals, x);
+      dequant16(v[b], sv[b], x);
+      store16(vo + i * kVals, x);
+    }
   }
 }
 

@@ -90,9 +90,9 @@ cudaError_t launch_q8_portable(const StepArgs& a, const Q8Cache& c, cudaStream_t
 constexpr int kDequantMaxEntries = 128;
 
 // Logical pages first .. first + n - 1 of request r become destination pages dst .. dst + n - 1,
-// and table[row + first + i] = dst + i.
+// and table[row + first + i] = dst + i. Positions before first_pos are read as zeros.
 struct DequantEntry {
-  int r, first, n, dst, row;
+  int r, first, n, dst, row, first_pos;
 };
 
 struct DequantArgs {

@@ -365,9 +365,9 @@ cudaError_t run_chunks(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c
     for (int j = 0; j < n; ++j) {
       cb::PrefillEntry e = plan.chunks[i + j];
       const int all = (e.seq_len + a.block_size - 1) / a.block_size;
-      const int first =
-          first_key(e.seq_len - e.q_len, a.sliding_window) / 128 * 128 / a.block_size;
-      d.entries[j] = cb::DequantEntry{e.r, first, all - first, dst, row};
+      const int first_pos = first_key(e.seq_len - e.q_len, a.sliding_window);
+      const int first = first_pos / 128 * 128 / a.block_size;
+      d.entries[j] = cb::DequantEntry{e.r, first, all - first, dst, row, first_pos};
       int splits = 1;
       if (per > 0) {
         splits = entry_splits(e, TQ, a.sliding_window, per);

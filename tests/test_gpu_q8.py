@@ -293,6 +293,23 @@ def test_values_of_unattended_slots_do_not_matter(q, dtype):
     assert torch.equal(st.run(), clean)
 
 
+@pytest.mark.parametrize("ctx", [500, 5000])
+@pytest.mark.parametrize("W,BS", [(0, 16), (30, 16), (150, 128)])
+def test_values_of_unattended_slots_do_not_matter_to_chunks(W, BS, ctx):
+    spec = spec_of([200, 70], [ctx, 37], sliding_window=W, block_size=BS, seed=2)
+    st = Q8Step(spec, seed=1)
+    clean = st.run().clone()
+    used = np.zeros(spec.num_blocks * BS, bool)
+    for r in range(spec.R):
+        first = max(0, int(spec.ctx_lens[r]) - W + 1) if W else 0
+        for p in range(first, int(spec.seq_lens[r])):
+            used[spec.block_table[r, p // BS] * BS + p % BS] = True
+    keep = torch.from_numpy(used).cuda().view(spec.num_blocks, BS)
+    for i in range(4):
+        st.d[i][~keep] = 0x7F if i < 2 else 0xFF
+    assert torch.equal(st.run(), clean)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rows_of_very_different_scale(dtype):
     """K rows from 2^-20 to 2^6 and V rows from 2^-60 to 2^60 in one context: the weights of the
