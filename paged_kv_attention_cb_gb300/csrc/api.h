@@ -11,6 +11,13 @@ namespace cb {
 cb_status report_error(cb_status s, const char* msg);
 cb_status report_cuda_error(cudaError_t e, const char* what);
 
+// Arrays in a workspace start at multiples of 32 bytes whatever the workspace's own address (16-byte
+// aligned): the widest stores take 32. A workspace has kWorkspaceAlign bytes to spare for it.
+constexpr size_t kWorkspaceAlign = 32;
+inline uint8_t* align_workspace(void* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + kWorkspaceAlign - 1) & ~(uintptr_t)(kWorkspaceAlign - 1));
+}
+
 inline bool is_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The sizes of a step: signs, supported head_dim / group / block_size / dtype, host mirrors given.

@@ -453,7 +453,7 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
                                       h_query_start_loc, h_seq_lens);
   if (st != CB_OK) return st;
   Layout w = layout_of(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim, false);
-  if (!workspace || workspace_bytes < w.scratch)
+  if (!workspace || workspace_bytes < w.scratch + cb::kWorkspaceAlign)
     return report_error(CB_ERR_WORKSPACE, "workspace missing or smaller than cb_workspace_size_q8()");
   if (!cb::is_aligned16(workspace))
     return report_error(CB_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
@@ -499,7 +499,8 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
   // (which also takes head counts whose blocks' scales would fill the ring)
   const bool fast = block_size % cb::kQ8KeyBlock == 0 && num_kv_heads <= 128 &&
                     !(flags & CB_FLAG_PORTABLE_ONLY);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = cb::align_workspace(workspace);
+  workspace_bytes -= cb::kWorkspaceAlign;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   static thread_local Q8Plan plan;  // its vectors keep their storage from call to call
   plan.split = false;
@@ -595,7 +596,7 @@ size_t cb_workspace_size_q8(int32_t num_requests, int32_t num_tokens, int32_t nu
       block_size <= 0)
     return cb::kWorkspaceHeaderBytes;
   const size_t fixed = layout_of(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim,
-                                 chunk_kv_tokens > 0).scratch;
+                                 chunk_kv_tokens > 0).scratch + cb::kWorkspaceAlign;
   if (chunk_kv_tokens <= 0) return fixed;
   // each request's pages are rounded up
   const int64_t pages = chunk_kv_tokens / block_size + std::min<int64_t>(num_requests, chunk_kv_tokens);

@@ -37,7 +37,7 @@ size_t partial_entries(int64_t R, int64_t T, int64_t Hq) {
 
 size_t shared_bytes(int64_t R, int64_t T, int64_t Hq, int64_t D) {
   const size_t n = partial_entries(R, T, Hq);
-  return cb::kWorkspaceHeaderBytes + align256(n * 8) + n * D * 4;
+  return cb::kWorkspaceHeaderBytes + cb::kWorkspaceAlign + align256(n * 8) + n * D * 4;
 }
 
 // Measured on GB300 (32 and 16 rows of 64 query heads behind 131072 positions of 8 KV heads: 106.4
@@ -245,7 +245,7 @@ bool plan_shared(SharedPlan& sp, const cb::StepArgs& a, const int32_t* qsl, cons
   for (const Group& g : sp.groups) rows += (size_t)partial_rows(g, per);
   if ((slots + rows) * a.num_q_heads > entries) return false;
   cb::plan_decode(plan, a, qsl, seq, prefix, U, C, scatter);
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = cb::align_workspace(workspace);
   plan.decode.part_ml = reinterpret_cast<float2*>(ws + cb::kWorkspaceHeaderBytes);
   plan.decode.part_o = reinterpret_cast<float*>(ws + cb::kWorkspaceHeaderBytes + align256(entries * 8));
   plan_prefix(sp, a, per, S, (int)slots);

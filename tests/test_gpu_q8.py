@@ -310,6 +310,34 @@ def test_values_of_unattended_slots_do_not_matter_to_chunks(W, BS, ctx):
     assert torch.equal(st.run(), clean)
 
 
+def shifted(t):
+    """The same tensor 16 bytes behind an address that is a multiple of 256."""
+    flat = torch.empty(t.numel() + 16 // t.element_size(), dtype=t.dtype, device=t.device)
+    return flat[16 // t.element_size():].view(t.shape).copy_(t)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("q,ctx", [([1, 1, 1], [700, 20, 3000]), ([1, 200, 3], [700, 4000, 50])])
+def test_addresses_aligned_to_sixteen_bytes(q, ctx, dtype):
+    st = Q8Step(spec_of(q, ctx, dtype=dtype, seed=4), seed=4)
+    st.d = [shifted(t) for t in st.d]
+    st.dq, st.dk, st.dv, st.ws = (shifted(t) for t in (st.dq, st.dk, st.dv, st.ws))
+    st.check(st.run(out=shifted(torch.full_like(st.dq, float("nan")))))
+    st.check_cache()
+    k, v = torch.empty_like(st.dk), torch.empty_like(st.dv)
+    cb.read_kv_q8(*st.d, st.md["slot_mapping"], shifted(k), shifted(v))
+
+
+@pytest.mark.parametrize("Hkv,portable", [(7, False), (11, False), (128, False), (129, True)])
+def test_any_number_of_heads(Hkv, portable):
+    """Heads that a CTA's eight do not divide, the most the tensor-core kernel takes, and more."""
+    i = cb.kernel_names().index("portable_q8")
+    before = cb.launch_count(i)
+    st = Q8Step(spec_of([1, 4, 70], [90, 33, 40], num_q_heads=Hkv, num_kv_heads=Hkv, head_dim=64, seed=4), seed=4)
+    st.check(st.run())
+    assert cb.launch_count(i) == before + portable
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rows_of_very_different_scale(dtype):
     """K rows from 2^-20 to 2^6 and V rows from 2^-60 to 2^60 in one context: the weights of the

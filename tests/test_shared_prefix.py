@@ -237,6 +237,20 @@ def test_a_workspace_serves_steps_of_any_size_and_replays():
 
 
 @pytest.mark.gpu
+def test_addresses_aligned_to_sixteen_bytes():
+    def shifted(t):
+        flat = torch.empty(t.numel() + 16 // t.element_size(), dtype=t.dtype, device=t.device)
+        return flat[16 // t.element_size():].view(t.shape).copy_(t)
+
+    st = Step([(512, [3] * 40), (1024, [70, 2])], extra_q=[(300, 100)], seed=1)
+    st.x = {k: shifted(v) for k, v in st.x.items()}
+    st.ws = shifted(st.ws)
+    before = prefix_launches()
+    st.check(st.run(out=shifted(torch.full_like(st.x["q"], float("nan")))))
+    assert prefix_launches() == before + 1
+
+
+@pytest.mark.gpu
 def test_bad_prefix_page_is_recorded():
     st = Step([(256, [3, 9])], seed=2)
     st.md["block_table"][0, 3] = st.spec.num_blocks + 1
