@@ -21,8 +21,9 @@ using cb::report_error;
 constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Requests of more query columns (tokens x grouped heads) than this are prefilled: their pages
-// are turned into bf16 once and the tcgen05 tiles read those. Below it the split kernel reads
-// the 8-bit pages directly, once per 64 columns.
+// are turned into bf16 once and the tcgen05 tiles read those. Below it, and where they are small
+// (kSmallRunBlocks), the split kernel reads the 8-bit pages directly, once per item of up to 64
+// columns (16 runs of 17 tokens behind 2000 positions, 32/8 heads: 76 us as chunks, 111 split).
 constexpr int kChunkColumns = 64;
 
 // How a CTA's consumer warps divide the work on items of up to `columns` query columns: 16 warps
@@ -48,6 +49,19 @@ Split split_of(int64_t columns, int Hkv) {
 }
 
 int tokens_per_item(const Split& s, int G) { return 8 * s.column_blocks * s.column_warps / G; }
+
+// What a key block costs with items of 8, 16, 32 and 64 columns (64 requests of 128 .. 2048
+// positions, 32/8 heads of 128, runs of 2, 4, 8 and 16 tokens: 38.5, 41.8, 71.6 and 131.7 us, of
+// which 9 are not the blocks'). Wider items convert the same keys in every column warp, so that
+// they save little but the reading: a run of 10 tokens between 63 decode rows took 118 us as one
+// item of 64 columns, and the decode rows with it, against 36 as five of 8.
+constexpr double kBlockCost[4] = {1.0, 1.12, 2.13, 4.17};
+
+// Longer runs of at most this many key blocks in items of 16 columns (of 8 heads of 128, all runs
+// together) stay in the split kernel: ~10 us of its time, what the pages' copy and the start of the
+// tiles take (one run of 17 tokens behind 2000 positions: 22 us as a chunk, 15 here; behind 16000: 45
+// and 57; 20 tokens behind 1000 beside 63 decode rows: 53 us and 36).
+constexpr int64_t kSmallRunBlocks = 1700;
 
 // Units that chunks are split into, at most (a second round of the SMs gains nothing that the first
 // does not have); pieces of a row, at most; and what a unit costs (microseconds of one SM): a
@@ -118,6 +132,22 @@ struct Q8Plan {
 
 int first_key(int pos0, int window) { return window > 0 ? std::max(0, pos0 - window + 1) : 0; }
 
+// Key blocks of the items of `tokens` query tokens of the requests with min_q <= q_len <= max_q, each
+// item counted with `more` besides (up to `limit`).
+int64_t split_blocks(const cb::StepArgs& a, const int32_t* qsl, const int32_t* seq_lens, int min_q, int max_q,
+                     int tokens, int more, int64_t limit) {
+  int64_t sum = 0;
+  for (int r = 0; r < a.num_requests && sum <= limit; ++r) {
+    const int q = qsl[r + 1] - qsl[r];
+    if (q < min_q || q > max_q) continue;
+    for (int t = 0; t < q && sum <= limit; t += tokens) {
+      const int pos0 = seq_lens[r] - q + t, last = seq_lens[r] - q + std::min(q, t + tokens) - 1;
+      sum += last / cb::kQ8KeyBlock - first_key(pos0, a.sliding_window) / cb::kQ8KeyBlock + 1 + more;
+    }
+  }
+  return sum;
+}
+
 // The split kernel's launch over the requests with 1 <= q_len <= max_q.
 void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int max_q,
                 const int32_t* qsl, const int32_t* seq_lens, const Layout& w, uint8_t* ws) {
@@ -130,7 +160,19 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
   if (longest == 0) return;
   plan.split = true;
   plan.decode_only = longest == 1 && plan.chunks.empty();
-  const Split sp = split_of((int64_t)longest * G, a.num_kv_heads);
+  Split sp = {};
+  double best = 0.0;
+  for (int i = 0; i < 4; ++i) {  // the items' columns
+    const int columns = 8 << i;
+    if (columns < G) continue;
+    const Split s = split_of(columns, a.num_kv_heads);
+    const double cost = kBlockCost[i] * (double)split_blocks(a, qsl, seq_lens, 1, max_q, columns / G, kPieceBlocks, INT64_MAX);
+    if (best == 0.0 || cost < best) {
+      best = cost;
+      sp = s;
+    }
+    if (columns >= (int64_t)longest * G) break;
+  }
   plan.column_blocks = sp.column_blocks;
 
   cb::Q8Args& p = plan.args;
@@ -511,14 +553,22 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
   plan.max_pieces = 0;
   if (fast) {
     const int G = num_q_heads / num_kv_heads;
-    const int max_q = dtype == CB_F32 ? INT_MAX : std::max(1, kChunkColumns / G);
+    int max_q = dtype == CB_F32 ? INT_MAX : std::max(1, kChunkColumns / G);
     const size_t need = plan_chunks(plan, a, max_q, h_query_start_loc, h_seq_lens);
     if (need > 0) w = layout_of(num_requests, num_tokens, num_q_heads, num_kv_heads, head_dim, true);
     if (w.scratch > workspace_bytes || need > workspace_bytes - w.scratch)
       return report_error(CB_ERR_WORKSPACE,
                           "workspace too small for the step's chunks: chunk_kv_tokens of "
                           "cb_workspace_size_q8() must cover the seq_lens of requests with q_len > 1");
-    if (need > 0) split_chunks(plan, a, w.chunk_entries);
+    if (need > 0) {
+      const int64_t limit = kSmallRunBlocks * 8 * 128 / ((int64_t)num_kv_heads * head_dim);
+      if (split_blocks(a, h_query_start_loc, h_seq_lens, max_q + 1, INT_MAX, 16 / G, 0, limit) <= limit) {
+        plan.chunks.clear();
+        max_q = INT_MAX;
+      } else {
+        split_chunks(plan, a, w.chunk_entries);
+      }
+    }
     plan_split(plan, a, c, max_q, h_query_start_loc, h_seq_lens, w, ws);
   }
   cudaError_t e = cudaSuccess;

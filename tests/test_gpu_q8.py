@@ -225,6 +225,18 @@ def test_query_runs(Hq, Hkv, D, BS, dtype):
     st.check_cache()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (8, 2, 64), (16, 1, 128)])
+@pytest.mark.parametrize("columns", [16, 32, 64])
+def test_runs_of_one_length(columns, Hq, Hkv, D, dtype):
+    """Drafts of every request: items of each width."""
+    n = columns * Hkv // Hq
+    st = Q8Step(spec_of([n] * 5, [0, 31, 300, 1500, 90], num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D,
+                        dtype=dtype, seed=1), seed=2)
+    st.check(st.run())
+    st.check_cache()
+
+
 @pytest.mark.parametrize("dtype,W", [("bf16", 0), ("bf16", 150), ("f32", 0)])
 @pytest.mark.parametrize("Hq,Hkv,D,BS", [(8, 2, 128, 16), (4, 4, 64, 128), (16, 1, 64, 256)])
 def test_chunks_and_decodes(Hq, Hkv, D, BS, dtype, W):
@@ -235,22 +247,39 @@ def test_chunks_and_decodes(Hq, Hkv, D, BS, dtype, W):
     assert cb.read_error_word(st.ws) == 0
 
 
+def launches(name):
+    return cb.launch_count(cb.kernel_names().index(name))
+
+
+@pytest.mark.parametrize("W", [0, 600])
+@pytest.mark.parametrize("Hq,Hkv,D,BS", [(32, 8, 128, 16), (16, 16, 128, 128), (32, 16, 64, 32), (16, 1, 64, 256)])
+def test_long_chunks_and_decodes(Hq, Hkv, D, BS, W):
+    """Runs that are computed from bf16 copies of their pages, between decode rows (with one KV head
+    and a window they are little work, and stay with the decode rows)."""
+    st = Q8Step(spec_of([1, 530, 1, 257, 170], [90, 0, 400, 1333, 2128], num_q_heads=Hq, num_kv_heads=Hkv,
+                        head_dim=D, block_size=BS, sliding_window=W, seed=6), seed=3)
+    before = launches("dequant_pages")
+    st.check(st.run())
+    st.check_cache()
+    assert launches("dequant_pages") == before + (Hkv > 1 or W == 0)
+    assert cb.read_error_word(st.ws) == 0
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,BS,W,q,ctx", [
-    (8, 2, 128, 16, 0, [200], [5000]),             # three pairs of query tiles and a tail
-    (4, 4, 64, 128, 0, [129, 1, 70], [2900, 800, 6001]),
-    (16, 1, 64, 32, 0, [30, 5], [7000, 12000]),    # two full tiles; a tail of five tokens
-    (8, 2, 128, 16, 1500, [257], [9000]),
-    (8, 2, 128, 256, 0, [512, 65], [0, 4000]),     # pairs of one and of many units
+    (8, 2, 128, 16, 0, [200], [15000]),            # three pairs of query tiles and a tail
+    (4, 4, 64, 128, 0, [129, 1, 70], [12900, 800, 16001]),
+    (16, 1, 64, 32, 0, [30, 5], [37000, 42000]),   # two full tiles; a tail of five tokens
+    (8, 2, 128, 16, 5500, [257], [9000]),
+    (8, 2, 128, 256, 0, [512, 65], [3000, 14000]),  # pairs of one and of many units
 ])
 def test_few_chunks_behind_long_contexts(Hq, Hkv, D, BS, W, q, ctx):
     """The keys of too few query tiles to fill the GPU are split; the pieces are merged."""
     st = Q8Step(spec_of(q, ctx, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D, block_size=BS,
                         sliding_window=W, seed=6), seed=3)
-    i = cb.kernel_names().index("merge_rows")
-    before = cb.launch_count(i)
+    before = launches("merge_rows"), launches("dequant_pages")
     st.check(st.run())
     st.check_cache()
-    assert cb.launch_count(i) > before
+    assert launches("merge_rows") > before[0] and launches("dequant_pages") == before[1] + 1
     assert cb.read_error_word(st.ws) == 0
 
 
@@ -293,12 +322,14 @@ def test_values_of_unattended_slots_do_not_matter(q, dtype):
     assert torch.equal(st.run(), clean)
 
 
-@pytest.mark.parametrize("ctx", [500, 5000])
-@pytest.mark.parametrize("W,BS", [(0, 16), (30, 16), (150, 128)])
+@pytest.mark.parametrize("ctx", [500, 15000])
+@pytest.mark.parametrize("W,BS", [(0, 16), (30, 16), (60, 16), (150, 128)])
 def test_values_of_unattended_slots_do_not_matter_to_chunks(W, BS, ctx):
-    spec = spec_of([200, 70], [ctx, 37], sliding_window=W, block_size=BS, seed=2)
+    spec = spec_of([2000, 70], [ctx, 37], sliding_window=W, block_size=BS, seed=2)
     st = Q8Step(spec, seed=1)
+    before = launches("dequant_pages")
     clean = st.run().clone()
+    assert launches("dequant_pages") == before + (W != 30)  # (a small window: little work)
     used = np.zeros(spec.num_blocks * BS, bool)
     for r in range(spec.R):
         first = max(0, int(spec.ctx_lens[r]) - W + 1) if W else 0
@@ -379,8 +410,8 @@ def test_bad_page_ids_read_as_zeros():
 
 
 def test_steps_of_any_size_share_a_workspace():
-    ws = cb.alloc_workspace_q8(64, 600, 32, 8, 128, 16, 2000)
-    for q, ctx in (([1] * 40, list(range(0, 1200, 30))), ([1], [3000]), ([300, 1, 4], [500, 800, 20]), ([1] * 3, [9, 90, 900])):
+    ws = cb.alloc_workspace_q8(64, 600, 32, 8, 128, 16, 6000)
+    for q, ctx in (([1] * 40, list(range(0, 1200, 30))), ([1], [3000]), ([300, 1, 4], [5000, 800, 20]), ([300, 1, 4], [500, 800, 20]), ([1] * 3, [9, 90, 900])):
         st = Q8Step(spec_of(q, ctx, seed=len(q)), seed=len(q))
         st.check(st.run(ws=ws))
     assert cb.read_error_word(ws) == 0
@@ -395,8 +426,9 @@ def test_many_requests_and_many_pieces():
     st.check(st.run())
 
 
-def test_graph_replay_and_side_stream():
-    st = Q8Step(spec_of([1, 3, 100], [700, 50, 20], seed=3), seed=3)
+@pytest.mark.parametrize("q,ctx", [([1, 3, 100], [700, 50, 20]), ([1, 3, 200], [700, 50, 6000])])
+def test_graph_replay_and_side_stream(q, ctx):
+    st = Q8Step(spec_of(q, ctx, seed=3), seed=3)
     s = torch.cuda.Stream()
     out = torch.full_like(st.dq, float("nan"))
     with torch.cuda.stream(s):
