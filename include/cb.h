@@ -404,8 +404,7 @@ cb_status cb_read_kv_q8(const void* k_cache, const void* v_cache, const void* k_
  * with q_len > 1 of one step have together; 0 for steps of decode rows only (and for fp32
  * steps, which need no scratch for them). Long query runs (more than 64 query columns, tokens
  * times the group size) are computed from a bf16 copy of their requests' pages, which lives
- * there for the step: 4 Hkv D bytes a position, beside partial results of up to 400 (Hq D)
- * rows a token or 50 MB.
+ * there for the step: 4 Hkv D bytes a position, and at most 51 MB of partial results.
  * The workspace is initialised with cb_workspace_init and its error word read with
  * cb_read_error_word, as cb_paged_attention's.
  */

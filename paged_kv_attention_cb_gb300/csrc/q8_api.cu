@@ -670,7 +670,7 @@ cb_status cb_paged_attention_q8(void* out, const void* q, void* k_cache, void* v
                         h_query_start_loc, h_seq_lens, num_requests, num_tokens, num_blocks,
                         block_size, num_q_heads, num_kv_heads, head_dim, scale, sliding_window,
                         dtype, flags, workspace, workspace_bytes, stream);
-  } catch (...) {  // host memory ran out while planning; nothing was launched
+  } catch (...) {  // host memory ran out while planning (some of the step may be launched)
     return report_error(CB_ERR_INVALID_ARG, "out of host memory");
   }
 }

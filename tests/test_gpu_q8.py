@@ -265,6 +265,14 @@ def test_long_chunks_and_decodes(Hq, Hkv, D, BS, W):
     assert cb.read_error_word(st.ws) == 0
 
 
+def test_more_chunks_than_one_launch_lists():
+    st = Q8Step(spec_of([70, 90] * 65, [60, 100] * 65, num_q_heads=8, num_kv_heads=2, head_dim=64, seed=1), seed=1)
+    before = launches("dequant_pages")
+    st.check(st.run())
+    st.check_cache()
+    assert launches("dequant_pages") == before + 2
+
+
 @pytest.mark.parametrize("Hq,Hkv,D,BS,W,q,ctx", [
     (8, 2, 128, 16, 0, [200], [15000]),            # three pairs of query tiles and a tail
     (4, 4, 64, 128, 0, [129, 1, 70], [12900, 800, 16001]),
