@@ -47,8 +47,8 @@
 //   CTA has that many fewer heads), so that the cache is still read once; or the run is several
 //   items of fewer columns, which read it again (the planner chooses per step).
 // Measured (32/8 heads of 128 unless said): 16 requests of 32768 positions, 64/8 heads: 162 us, 98 %
-// of the copy rate; 64 requests of 128 .. 2048: 31.6 us for 141 MB, of which ~9 us are start, pieces'
-// ends and merge; the same with runs of 4 tokens 41.8 us, fp32 55.8; 4 requests of up to 301: 8.6 us.
+// of the copy rate; 64 requests of 128 .. 2048: 30.4 us for 141 MB, of which ~8 us are start, pieces'
+// ends and merge; the same with runs of 4 tokens 41.8 us, fp32 55.8; 4 requests of up to 301: 7.3 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <float.h>
