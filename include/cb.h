@@ -419,7 +419,9 @@ size_t cb_workspace_size_q8(int32_t num_requests, int32_t num_tokens, int32_t nu
  * does; attention reads them back from the cache, so a row's own position takes part with its
  * stored value. Then, with K_p and V_p the stored values (e4m3 times scale),
  *     out[t, h] = sum_p softmax_p(scale * <q[t, h], K_p[g]>) * V_p[g]
- * over the positions of cb_paged_attention, accumulated in fp32 and rounded to the dtype of q.
+ * over the positions of cb_paged_attention, accumulated in fp32 and rounded to the dtype of q. The
+ * product of a softmax weight and V's scale is kept to 2^-11 of itself (fp32: 2^-21; in long bf16
+ * runs the weight to 2^-8) or to 2^-31 of the row's largest such product, whichever is more.
  * Arguments, metadata, host mirrors, errors and flags are cb_paged_attention's (dtype is that
  * of q, out, k_new and v_new; CB_FLAG_PORTABLE_ONLY is honoured), with the two scale arrays
  * after the caches. Scale bytes of attended rows lie in 1 .. 254.

@@ -27,7 +27,8 @@
 //   scaled per row by a power of two to a largest magnitude in [2^13, 2^14): a bf16 row is
 //   then exact down to 2^-38 of its largest element, and an fp32 row is the sum of two fp16
 //   rows to 2^-22. Weights are fp16 (bf16 queries: 11 bits, finer than the bf16 the output is
-//   rounded to) or the sum of two fp16 (fp32 queries), scaled to at most 2^14.
+//   rounded to) or the sum of two fp16 (fp32 queries), scaled to at most 2^14 and, with the
+//   maximum just raised, 2^6: the smallest are rounded to 2^-25, 2^-31 of the largest.
 // * Layout. Keys are the M = 16 rows of both products' A operand side, columns the N = 8.
 //   The contraction index may be permuted freely, so a lane takes its operands from whole
 //   16-byte pieces of the staged rows: for S^T = K Q^T lane (g, t) holds d = D/4 t ..
