@@ -22,7 +22,7 @@ constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Requests of more query columns (tokens x grouped heads) than this are prefilled: their pages
 // are turned into bf16 once and the tcgen05 tiles read those. Below it, and where they are small
-// (kSmallRunBlocks), the split kernel reads the 8-bit pages directly, once per item of up to 64
+// (small_run_blocks), the split kernel reads the 8-bit pages directly, once per item of up to 64
 // columns (16 runs of 17 tokens behind 2000 positions, 32/8 heads: 76 us as chunks, 111 split).
 constexpr int kChunkColumns = 64;
 
@@ -59,11 +59,13 @@ int tokens_per_item(const Split& s, int G) { return 8 * s.column_blocks * s.colu
 // 128, runs of 8 tokens: 88, 50, 37 and 31 us with items of 8, 16, 32 and 64).
 constexpr double kBlockCost[2][4] = {{1.0, 1.12, 2.13, 4.17}, {0.8, 1.12, 1.6, 2.3}};
 
-// Longer runs of at most this many key blocks in items of 16 columns (of 8 heads of 128, all runs
-// together) stay in the split kernel: ~10 us of its time, what the pages' copy and the start of the
-// tiles take (one run of 17 tokens behind 2000 positions: 22 us as a chunk, 15 here; behind 16000: 45
-// and 57; 20 tokens behind 1000 beside 63 decode rows: 53 us and 36).
-constexpr int64_t kSmallRunBlocks = 1700;
+// Longer runs of at most this many key blocks in items of 16 columns (all runs together) stay in the
+// split kernel: ~12 us of its time, what the pages' copy and the start of the tiles take (one run of
+// 17 tokens behind 2000 positions, 32/8 heads of 128: 22 us as a chunk, 15 here; behind 16000: 45 and
+// 57; 20 tokens behind 1000 beside 63 decode rows: 53 and 35). Blocks of fewer or narrower heads
+// cost less, but not in proportion: the two meet at ~2200 blocks of 1024 values, 5500 of 256, 9500 of
+// 128 and 16000 of 64.
+int64_t small_run_blocks(int Hkv, int D) { return (int64_t)(2200.0 * pow(1024.0 / ((double)Hkv * D), 0.7)); }
 
 // Units that chunks are split into, at most (a second round of the SMs gains nothing that the first
 // does not have); pieces of a row, at most; and what a unit costs (microseconds of one SM): a
@@ -566,7 +568,7 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
                           "workspace too small for the step's chunks: chunk_kv_tokens of "
                           "cb_workspace_size_q8() must cover the seq_lens of requests with q_len > 1");
     if (need > 0) {
-      const int64_t limit = kSmallRunBlocks * 8 * 128 / ((int64_t)num_kv_heads * head_dim);
+      const int64_t limit = small_run_blocks(num_kv_heads, head_dim);
       if (split_blocks(a, h_query_start_loc, h_seq_lens, max_q + 1, INT_MAX, 16 / G, 0, limit) <= limit) {
         plan.chunks.clear();
         max_q = INT_MAX;
