@@ -977,20 +977,27 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
 
 // ------------------------------------------------------------------ portable kernel
 //
-// One warp per (query row, KV head): walks the row's positions in order with a running
-// (max, sum, output) in fp32, as the portable kernel of the bf16/fp32 cache. For block sizes
-// below 16 (a key block of the split kernel must lie in one page).
+// One CTA per (query row, KV head), for block sizes below 16 (a key block of the split kernel must
+// lie in one page) and more KV heads than its ring's scales allow. Its warps take the row's
+// positions a few at a time in turn, each with a running (max, sum, output) in fp32 per query head of
+// the group, and join through shared memory at the end. Bound by the loads' latency, so a warp has
+// those of four positions in flight (one warp with one position: 2443 us for one request of 4000
+// positions in pages of 8, 32/8 heads).
+
+constexpr int kPortableWarps = 8;
+constexpr int kPortableKeys = 4;
 
 template <typename T, int VPT, int G>
-__global__ void __launch_bounds__(128) q8_portable_kernel(StepArgs a, Q8Cache c) {
+__global__ void __launch_bounds__(kPortableWarps * 32) q8_portable_kernel(StepArgs a, Q8Cache c) {
+  constexpr int D = VPT * 32;
+  __shared__ float sh_o[kPortableWarps][D];
+  __shared__ float2 sh_ml[kPortableWarps];
   grid_dependency_wait();
   allow_dependent_launch();
-  const int lane = threadIdx.x & 31;
-  const int64_t idx = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int Hkv = a.num_kv_heads;
-  if (idx >= (int64_t)a.num_tokens * Hkv) return;
-  const int t = (int)(idx / Hkv);
-  const int g = (int)(idx % Hkv);
+  const int t = (int)(blockIdx.x / Hkv);
+  const int g = (int)(blockIdx.x % Hkv);
   int lo_r = 0, hi_r = a.num_requests;
   while (hi_r - lo_r > 1) {
     const int mid = (lo_r + hi_r) >> 1;
@@ -1001,7 +1008,6 @@ __global__ void __launch_bounds__(128) q8_portable_kernel(StepArgs a, Q8Cache c)
   const int q_len = __ldg(a.query_start_loc + r + 1) - q_start;
   const int last = __ldg(a.seq_lens + r) - q_len + (t - q_start);
   const int first = first_key(last, a.sliding_window);
-  constexpr int D = VPT * 32;
   const T* q = static_cast<const T*>(a.q) + ((int64_t)t * a.num_q_heads + g * G) * D + lane * VPT;
   float qv[G][VPT], m[G], l[G], o[G][VPT];
 #pragma unroll
@@ -1015,47 +1021,81 @@ __global__ void __launch_bounds__(128) q8_portable_kernel(StepArgs a, Q8Cache c)
     }
   }
   const int32_t* bt = a.block_table + (int64_t)r * a.bt_stride;
-  for (int p = first; p <= last; ++p) {
-    const int blk = __ldg(bt + bt_entry(p / a.block_size, a.ring_blocks));
-    const bool ok = blk >= 0 && blk < a.num_blocks;
-    if (!ok && lane == 0) record_error(a.error_word, CB_DEVERR_BLOCK_ID);
-    const int64_t row = ok ? ((int64_t)blk * a.block_size + p % a.block_size) * Hkv + g : 0;
-    float kv[VPT], vv[VPT];
-    const float sk = ok ? e8m0_value(__ldg(c.k_scale + row)) : 0.f;
-    const float sv = ok ? e8m0_value(__ldg(c.v_scale + row)) : 0.f;
+  for (int64_t p0 = (int64_t)first + warp * kPortableKeys; p0 <= last; p0 += kPortableWarps * kPortableKeys) {
+    uint16_t kk[kPortableKeys][VPT / 2], xx[kPortableKeys][VPT / 2];
+    int kc[kPortableKeys], vc[kPortableKeys];
+    bool ok[kPortableKeys];
+    int64_t row[kPortableKeys];
 #pragma unroll
-    for (int v = 0; v < VPT; v += 2) {
-      const uint16_t kk = ok ? *reinterpret_cast<const uint16_t*>(c.k + row * D + lane * VPT + v) : 0;
-      const uint16_t xx = ok ? *reinterpret_cast<const uint16_t*>(c.v + row * D + lane * VPT + v) : 0;
-      const float2 fk = float2_of_f16x2(f16x2_of_e4m3x2(kk)), fv = float2_of_f16x2(f16x2_of_e4m3x2(xx));
-      kv[v] = fk.x * sk;
-      kv[v + 1] = fk.y * sk;
-      vv[v] = fv.x * sv;
-      vv[v + 1] = fv.y * sv;
+    for (int i = 0; i < kPortableKeys; ++i) {
+      const int p = (int)min(p0 + i, (int64_t)last);
+      const int blk = __ldg(bt + bt_entry(p / a.block_size, a.ring_blocks));
+      ok[i] = blk >= 0 && blk < a.num_blocks;
+      if (!ok[i] && lane == 0) record_error(a.error_word, CB_DEVERR_BLOCK_ID);
+      row[i] = ok[i] ? ((int64_t)blk * a.block_size + p % a.block_size) * Hkv + g : 0;
     }
 #pragma unroll
-    for (int h = 0; h < G; ++h) {
-      float s = 0.f;
+    for (int i = 0; i < kPortableKeys; ++i) {
+      kc[i] = __ldg(c.k_scale + row[i]);
+      vc[i] = __ldg(c.v_scale + row[i]);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) s = fmaf(qv[h][v], kv[v], s);
+      for (int v = 0; v < VPT / 2; ++v) {
+        kk[i][v] = *reinterpret_cast<const uint16_t*>(c.k + row[i] * D + lane * VPT + 2 * v);
+        xx[i][v] = *reinterpret_cast<const uint16_t*>(c.v + row[i] * D + lane * VPT + 2 * v);
+      }
+    }
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      s *= a.scale_log2;
-      const float mn = fmaxf(m[h], s);
-      const float alpha = exp2f(m[h] - mn);
-      const float pe = exp2f(s - mn);
-      l[h] = l[h] * alpha + pe;
+    for (int i = 0; i < kPortableKeys; ++i) {
+      if (p0 + i > last) break;
+      const float sk = e8m0_value(kc[i]), sv = e8m0_value(vc[i]);
+      float kv[VPT], vv[VPT];
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) o[h][v] = fmaf(o[h][v], alpha, pe * vv[v]);
-      m[h] = mn;
+      for (int v = 0; v < VPT / 2; ++v) {
+        const float2 fk = float2_of_f16x2(f16x2_of_e4m3x2(kk[i][v])), fv = float2_of_f16x2(f16x2_of_e4m3x2(xx[i][v]));
+        kv[2 * v] = ok[i] ? fk.x * sk : 0.f;  // (a page id out of range reads as zeros)
+        kv[2 * v + 1] = ok[i] ? fk.y * sk : 0.f;
+        vv[2 * v] = ok[i] ? fv.x * sv : 0.f;
+        vv[2 * v + 1] = ok[i] ? fv.y * sv : 0.f;
+      }
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        float s = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) s = fmaf(qv[h][v], kv[v], s);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        s *= a.scale_log2;
+        const float mn = fmaxf(m[h], s);
+        const float alpha = exp2f(m[h] - mn);
+        const float pe = exp2f(s - mn);
+        l[h] = l[h] * alpha + pe;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) o[h][v] = fmaf(o[h][v], alpha, pe * vv[v]);
+        m[h] = mn;
+      }
     }
   }
-  T* out = static_cast<T*>(a.out) + ((int64_t)t * a.num_q_heads + g * G) * D + lane * VPT;
+  T* out = static_cast<T*>(a.out) + ((int64_t)t * a.num_q_heads + g * G) * D;
 #pragma unroll
   for (int h = 0; h < G; ++h) {
-    const float inv = l[h] > 0.f ? 1.f / l[h] : (l[h] == l[h] ? 0.f : l[h]);  // a NaN stays one
+    __syncthreads();  // the head before has been read
+    if (lane == 0) sh_ml[warp] = make_float2(m[h], l[h]);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) out[h * D + v] = Elt<T>::from_f(o[h][v] * inv);
+    for (int v = 0; v < VPT; ++v) sh_o[warp][lane * VPT + v] = o[h][v];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      float M = -FLT_MAX, L = 0.f, x = 0.f;
+#pragma unroll
+      for (int w = 0; w < kPortableWarps; ++w) M = fmaxf(M, sh_ml[w].x);
+#pragma unroll
+      for (int w = 0; w < kPortableWarps; ++w) {
+        const float f = exp2f(sh_ml[w].x - M);
+        L += sh_ml[w].y * f;
+        x += sh_o[w][threadIdx.x] * f;
+      }
+      const float inv = L > 0.f ? 1.f / L : (L == L ? 0.f : L);  // a NaN stays one
+      out[h * D + threadIdx.x] = Elt<T>::from_f(x * inv);
+    }
   }
 }
 
@@ -1135,8 +1175,9 @@ cudaError_t launch_split_d(const Q8Args& p, int nb, cudaStream_t s) {
 
 template <typename T, int VPT>
 cudaError_t launch_portable_t(const StepArgs& a, const Q8Cache& c, cudaStream_t s) {
-  const int64_t warps = (int64_t)a.num_tokens * a.num_kv_heads;
-  const dim3 grid((unsigned)((warps + 3) / 4)), block(128);
+  const int64_t ctas = (int64_t)a.num_tokens * a.num_kv_heads;
+  if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)ctas), block(kPortableWarps * 32);
   switch (a.num_q_heads / a.num_kv_heads) {
     case 1: return launch_pdl(kPortableQ8, q8_portable_kernel<T, VPT, 1>, grid, block, 0, s, a, c);
     case 2: return launch_pdl(kPortableQ8, q8_portable_kernel<T, VPT, 2>, grid, block, 0, s, a, c);
