@@ -426,8 +426,8 @@ size_t cb_workspace_size_q8(int32_t num_requests, int32_t num_tokens, int32_t nu
  * of q, out, k_new and v_new; CB_FLAG_PORTABLE_ONLY is honoured), with the two scale arrays
  * after the caches. Scale bytes of attended rows lie in 1 .. 254.
  *
- * Block sizes that are multiples of 16 run on the tensor cores; smaller ones, and more than 128
- * KV heads, on the CUDA cores. Cache rows that no token of a request attends may hold anything. In
+ * Block sizes from 16 on, and of 8 with an even number of KV heads, run on the tensor cores; smaller
+ * ones, and more than 128 KV heads, on the CUDA cores. Cache rows that no token of a request attends may hold anything. In
  * long query runs (as above) a NaN in a V row that some tokens of the run attend may reach the
  * others of the run too.
  * CB_ERR_WORKSPACE where the workspace is smaller than cb_workspace_size_q8() says for the

@@ -18,7 +18,7 @@
 //   Each warp's share of an item in a CTA (a piece) becomes a partial row that the merge kernel
 //   joins (merge.h); only an item that one warp per head has to itself is written directly.
 // * Staging. Producer warps bring each block (16 keys, up to 8 KV heads, K and V) with two
-//   swizzled tensor copies, and its scales with two bulk copies, into a ring of stages. One
+//   swizzled tensor copies (four where a page has 8 keys), and its scales with two bulk copies, into a ring of stages. One
 //   warp needs ~0.5 us to place and issue a block, which bounded everything but the widest
 //   rows: four warps take the blocks in turn, and where blocks are small several lanes of
 //   each a block of their own at once.
@@ -53,6 +53,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <float.h>
+#include <limits.h>
 
 #include "cb.h"
 #include "common.cuh"
@@ -227,8 +228,11 @@ CB_DEV int blocks_of(int pos0, int ntok, int window) {
 
 }  // namespace
 
-// NB column blocks of 8; F32: fp32 queries and outputs (operands split into two fp16 parts).
-template <int D, int NB, bool F32>
+// NB column blocks of 8; F32: fp32 queries and outputs (operands split into two fp16 parts); P8: pages
+// of 8 keys (an instance of its own: with the offsets as variables the others spilled 104 bytes
+// instead of 76). 64 requests of 128 .. 2048 positions, 32/8 heads: 30.0 us in pages of 8 and 29.7 of
+// 16; on the portable kernel 365.
+template <int D, int NB, bool F32, bool P8>
 __global__ void __launch_bounds__(((NB == 1 ? 16 : 8) + kQ8Producers) * 32, 1)
 q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ Q8Args p) {
@@ -330,28 +334,51 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       qlen = __shfl_sync(0xffffffffu, w_q, j);
       seq = __shfl_sync(0xffffffffu, w_seq, j);
     };
-    // page ids of key blocks kb .. kb + n - 1 of the request (lane l: block kb + l)
+    // page ids of key blocks kb .. kb + n - 1 of the request (lane l: block kb + l); in pages of 8
+    // keys, pages2 has those of the blocks' second halves (kNoPage: past the request)
+    constexpr int kNoPage = INT_MIN;
+    int pages2 = kNoPage;
     auto load_pages = [&](int rr, int kb, int n) -> int {
-      return lane < n ? __ldg(p.a.block_table + (long long)rr * p.a.bt_stride +
-                              ((kb + lane) * kKB >> p.lg_block))
-                      : 0;
+      const int32_t* bt = p.a.block_table + (long long)rr * p.a.bt_stride;
+      if constexpr (P8)
+        pages2 = lane < n && ((kb + lane) * kKB + BS) < seq ? __ldg(bt + ((kb + lane) * 2 + 1)) : kNoPage;
+      return lane < n ? __ldg(bt + ((kb + lane) * kKB >> p.lg_block)) : 0;
     };
     // one lane: the copies of key block kb, in page pg, into stage st_i
-    auto copy_block = [&](int kb, int pg, int st_i) {
+    auto copy_block = [&](int kb, int pg, int pg2, int st_i) {
       const int key0 = (kb * kKB) & (BS - 1);
       uint64_t* const full = &sm.full[st_i];
       uint8_t* st = stages + st_i * stage_bytes;
       uint8_t* sc = scales + st_i * 2 * scale_bytes;
       const bool page_ok = pg >= 0 && pg < p.a.num_blocks;
-      if (!page_ok) record_error(p.a.error_word, CB_DEVERR_BLOCK_ID);
-      mbar_arrive_expect_tx(full, (uint32_t)(stage_bytes + (page_ok ? 2 * scale_bytes : 0)));
-      const int page = page_ok ? pg : p.a.num_blocks;  // past the pool: zeros
-      tma_load_4d_hint(st, &tmap_k, full, 0, key0, hg * HB, page, policy);
-      tma_load_4d_hint(st + box_bytes, &tmap_v, full, 0, key0, hg * HB, page, policy);
-      if (page_ok) {
-        const long long at = (((long long)pg << p.lg_block) + key0) * Hkv;
-        bulk_load(sc, p.c.k_scale + at, (uint32_t)scale_bytes, full);
-        bulk_load(sc + scale_bytes, p.c.v_scale + at, (uint32_t)scale_bytes, full);
+      if constexpr (P8) {  // 8 keys of each head from either page, one half of the stage behind the other
+        const bool ok2 = pg2 >= 0 && pg2 < p.a.num_blocks;
+        if (!page_ok || (!ok2 && pg2 != kNoPage)) record_error(p.a.error_word, CB_DEVERR_BLOCK_ID);
+        const uint32_t half = (uint32_t)scale_bytes / 2;
+        mbar_arrive_expect_tx(full, (uint32_t)stage_bytes + 2 * half * ((page_ok ? 1 : 0) + (ok2 ? 1 : 0)));
+        for (int h = 0; h < 2; ++h) {
+          const bool ok_h = h == 0 ? page_ok : ok2;
+          const int page = ok_h ? (h == 0 ? pg : pg2) : p.a.num_blocks;
+          tma_load_4d_hint(st + h * (box_bytes / 2), &tmap_k, full, 0, 0, hg * HB, page, policy);
+          tma_load_4d_hint(st + box_bytes + h * (box_bytes / 2), &tmap_v, full, 0, 0, hg * HB, page, policy);
+          if (ok_h) {
+            const long long at = ((long long)page << p.lg_block) * Hkv;
+            bulk_load(sc + h * half, p.c.k_scale + at, half, full);
+            bulk_load(sc + scale_bytes + h * half, p.c.v_scale + at, half, full);
+          }
+        }
+        return;
+      } else {
+        if (!page_ok) record_error(p.a.error_word, CB_DEVERR_BLOCK_ID);
+        mbar_arrive_expect_tx(full, (uint32_t)(stage_bytes + (page_ok ? 2 * scale_bytes : 0)));
+        const int page = page_ok ? pg : p.a.num_blocks;  // past the pool: zeros
+        tma_load_4d_hint(st, &tmap_k, full, 0, key0, hg * HB, page, policy);
+        tma_load_4d_hint(st + box_bytes, &tmap_v, full, 0, key0, hg * HB, page, policy);
+        if (page_ok) {
+          const long long at = (((long long)pg << p.lg_block) + key0) * Hkv;
+          bulk_load(sc, p.c.k_scale + at, (uint32_t)scale_bytes, full);
+          bulk_load(sc + scale_bytes, p.c.v_scale + at, (uint32_t)scale_bytes, full);
+        }
       }
     };
     bool more = u_lo < u_hi;
@@ -415,19 +442,20 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       const int u_end = u0 + nblk;
       for (int kb_base = first; kb_base < last && ok; kb_base += 32) {
         const int n = min(32, last - kb_base);
-        const int cur = pages;
+        const int cur = pages, cur2 = pages2;
         for (int j = 0, cnt; j < n; j += cnt) {
           if (GB == 1) {
             cnt = 1;
             if ((i & (kQ8Producers - 1)) == producer) {
               const int pg = __shfl_sync(0xffffffffu, cur, j);
+              const int pg2 = P8 ? __shfl_sync(0xffffffffu, cur2, j) : kNoPage;
               if ((round > 0 &&
                    !mbar_wait_warp_or_abort(&sm.empty[s], (uint32_t)(round - 1) & 1, &sm.abort_flag)) ||
                   *reinterpret_cast<volatile int*>(&sm.abort_flag)) {
                 ok = false;
                 break;
               }
-              if (lane == 0) copy_block(kb_base + j, pg, s);
+              if (lane == 0) copy_block(kb_base + j, pg, pg2, s);
               __syncwarp();
               issued_blocks = i + 1;
             }
@@ -436,6 +464,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if ((i / GB & (kQ8Producers - 1)) == producer) {
               // lane l < cnt: block j + l, stage s + l
               const int pg = __shfl_sync(0xffffffffu, cur, (j + lane) & 31);
+              const int pg2 = P8 ? __shfl_sync(0xffffffffu, cur2, (j + lane) & 31) : kNoPage;
               const bool mine = lane < cnt;
               const bool free = !mine || round == 0 ||
                                 mbar_wait_or_abort(&sm.empty[s + lane], (uint32_t)(round - 1) & 1, &sm.abort_flag);
@@ -443,7 +472,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 ok = false;
                 break;
               }
-              if (mine) copy_block(kb_base + j + lane, pg, s + lane);
+              if (mine) copy_block(kb_base + j + lane, pg, pg2, s + lane);
               __syncwarp();
               issued_blocks = i + cnt;
             }
@@ -524,11 +553,15 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
       // key_of_row(2 tq) at v_off, the next row of the fragment 128 bytes on with bit 4 of the
       // swizzled chunk turned, and the same two 8 keys further.
       const int key_a = key_of_row<D>(gid);
-      const uint32_t k_off = D == 128 ? row_chunk<D>(hl * kKB + key_a, 2 * tq)
-                                      : row_chunk<D>(hl * kKB + key_a, tq);
+      // this head's first staged row, and the bytes from a key's row to that of the key 8 further: in
+      // pages of 8 keys a block's halves lie behind one another with every head's 8 rows in each
+      const int row0 = hl * (P8 ? 8 : kKB);
+      const uint32_t next8 = (uint32_t)(8 * D * (P8 ? HB : 1));
+      const uint32_t k_off = D == 128 ? row_chunk<D>(row0 + key_a, 2 * tq)
+                                      : row_chunk<D>(row0 + key_a, tq);
       const uint32_t v_off =
-          box_bytes + (D == 128 ? row_chunk<D>(hl * kKB + key_of_row<D>(2 * tq), gid)
-                                : row_chunk<D>(hl * kKB + key_of_row<D>(2 * tq), gid >> 1) + (gid & 1) * 8);
+          box_bytes + (D == 128 ? row_chunk<D>(row0 + key_of_row<D>(2 * tq), gid)
+                                : row_chunk<D>(row0 + key_of_row<D>(2 * tq), gid >> 1) + (gid & 1) * 8);
       // this warp's query fragments: a lane's 8 bytes of each step, column block and fp16 part
       const uint32_t q_at = smem_u32(qfrags) + warp * q_frag_bytes(D, NB, F32) + lane * 8;
       int i0 = 0;                // block index of the piece's first block
@@ -687,7 +720,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
             if (f.row >= 0) {
               if (f.staged) {  // over the stale row in the staged block
                 const int key = d.pos0 - key_base;
-                const uint32_t at = row_chunk<D>(hl * kKB + key, w / 4) + (w & 3) * 4;
+                const uint32_t at = row_chunk<D>(row0 + (key & 7), w / 4) + (key >> 3) * next8 + (w & 3) * 4;
                 sts32(st + at, f.k[w]);
                 sts32(st + box_bytes + at, f.v[w]);
                 if (lane == 0) {
@@ -718,7 +751,7 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
           for (int half = 0; half < D / 64; ++half) {
             const uint4 va = lds128(st + (k_off ^ (half << 4)));
-            const uint4 vb = lds128(st + (k_off ^ (half << 4)) + 8 * D);
+            const uint4 vb = lds128(st + (k_off ^ (half << 4)) + next8);
             const uint32_t wa[4] = {va.x, va.y, va.z, va.w};
             const uint32_t wb[4] = {vb.x, vb.y, vb.z, vb.w};
 #pragma unroll
@@ -815,13 +848,13 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             if constexpr (D == 128) {
-              const uint4 x = lds128(st + (v_off ^ ((r & 1) << 4)) + (r & 1) * 128 + (r >> 1) * 8 * D);
+              const uint4 x = lds128(st + (v_off ^ ((r & 1) << 4)) + (r & 1) * 128 + (r >> 1) * next8);
               v[r][0] = x.x;
               v[r][1] = x.y;
               v[r][2] = x.z;
               v[r][3] = x.w;
             } else {
-              const uint2 x = lds64(st + (v_off ^ ((r & 1) << 4)) + (r & 1) * 128 + (r >> 1) * 8 * D);
+              const uint2 x = lds64(st + (v_off ^ ((r & 1) << 4)) + (r & 1) * 128 + (r >> 1) * next8);
               v[r][0] = x.x;
               v[r][1] = x.y;
             }
@@ -977,8 +1010,8 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
 
 // ------------------------------------------------------------------ portable kernel
 //
-// One CTA per (query row, KV head), for block sizes below 16 (a key block of the split kernel must
-// lie in one page) and more KV heads than its ring's scales allow. Its warps take the row's
+// One CTA per (query row, KV head), for block sizes below 8 (a key block of the split kernel lies in
+// one page or two), odd KV head counts in pages of 8, and more KV heads than its ring's scales allow. Its warps take the row's
 // positions a few at a time in turn, each with a running (max, sum, output) in fp32 per query head of
 // the group, and join through shared memory at the end. Bound by the loads' latency, so a warp has
 // those of four positions in flight (one warp with one position: 2443 us for one request of 4000
@@ -1124,7 +1157,7 @@ cudaError_t cache_map(CUtensorMap* map, void* cache, const StepArgs& a, int hb) 
   const cuuint64_t D = (cuuint64_t)a.head_dim, H = (cuuint64_t)a.num_kv_heads;
   cuuint64_t dims[4] = {D, (cuuint64_t)a.block_size, H, (cuuint64_t)a.num_blocks};
   cuuint64_t strides[3] = {H * D, D, (cuuint64_t)a.block_size * H * D};
-  cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)kKB, (cuuint32_t)hb, 1};
+  cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)(a.block_size < kKB ? a.block_size : kKB), (cuuint32_t)hb, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, cache, dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -1133,9 +1166,9 @@ cudaError_t cache_map(CUtensorMap* map, void* cache, const StepArgs& a, int hb) 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, int NB, bool F32>
+template <int D, int NB, bool F32, bool P8>
 cudaError_t launch_split_t(const Q8Args& p, cudaStream_t s) {
-  auto kern = q8_split_kernel<D, NB, F32>;
+  auto kern = q8_split_kernel<D, NB, F32, P8>;
   const int warps = p.heads_per_cta * p.key_warps * p.column_warps;
   const size_t smem = q8_smem_bytes(D, p.heads_per_cta, warps, NB, F32, p.stages, p.a.num_kv_heads);
   // a stage belongs to one producer and one key warp, which see every one of its phases
@@ -1161,14 +1194,14 @@ cudaError_t launch_split_t(const Q8Args& p, cudaStream_t s) {
                     mk, mv, p);
 }
 
-template <int D>
+template <int D, bool P8>
 cudaError_t launch_split_d(const Q8Args& p, int nb, cudaStream_t s) {
   if (p.a.dtype == CB_F32) {
-    if (nb == 1) return launch_split_t<D, 1, true>(p, s);
-    if (nb == 2) return launch_split_t<D, 2, true>(p, s);
+    if (nb == 1) return launch_split_t<D, 1, true, P8>(p, s);
+    if (nb == 2) return launch_split_t<D, 2, true, P8>(p, s);
   } else {
-    if (nb == 1) return launch_split_t<D, 1, false>(p, s);
-    if (nb == 2) return launch_split_t<D, 2, false>(p, s);
+    if (nb == 1) return launch_split_t<D, 1, false, P8>(p, s);
+    if (nb == 2) return launch_split_t<D, 2, false, P8>(p, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -1196,8 +1229,11 @@ size_t q8_smem_bytes(int D, int HB, int warps, int NB, bool f32, int stages, int
 }
 
 cudaError_t launch_q8_split(const Q8Args& p, int column_blocks, cudaStream_t stream) {
-  if (p.a.head_dim == 64) return launch_split_d<64>(p, column_blocks, stream);
-  return launch_split_d<128>(p, column_blocks, stream);
+  if (p.a.block_size == 8)
+    return p.a.head_dim == 64 ? launch_split_d<64, true>(p, column_blocks, stream)
+                              : launch_split_d<128, true>(p, column_blocks, stream);
+  return p.a.head_dim == 64 ? launch_split_d<64, false>(p, column_blocks, stream)
+                            : launch_split_d<128, false>(p, column_blocks, stream);
 }
 
 cudaError_t launch_q8_portable(const StepArgs& a, const Q8Cache& c, cudaStream_t stream) {

@@ -544,10 +544,11 @@ cb_status attention_q8(void* out, const void* q, const cb::Q8Cache& c, const voi
   a.dtype = dtype;
   a.error_word = static_cast<int32_t*>(workspace);
 
-  // a 16-key block lies in one page from block_size 16 on; the rest runs on the portable kernel
-  // (which also takes head counts whose blocks' scales would fill the ring)
-  const bool fast = block_size % cb::kQ8KeyBlock == 0 && num_kv_heads <= 128 &&
-                    !(flags & CB_FLAG_PORTABLE_ONLY);
+  // a 16-key block lies in one page, or in two of 8 keys, whose scales are copied in multiples of 16
+  // bytes; the rest runs on the portable kernel (which also takes head counts whose blocks' scales
+  // would fill the ring)
+  const bool fast = (block_size >= cb::kQ8KeyBlock || (block_size == 8 && num_kv_heads % 2 == 0)) &&
+                    num_kv_heads <= 128 && !(flags & CB_FLAG_PORTABLE_ONLY);
   uint8_t* ws = cb::align_workspace(workspace);
   workspace_bytes -= cb::kWorkspaceAlign;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -18,6 +18,10 @@ def cuda(a):
     return torch.from_numpy(np.ascontiguousarray(a)).cuda()
 
 
+def launches(name):
+    return cb.launch_count(cb.kernel_names().index(name))
+
+
 def host_rows(rng, shape, dtype):
     """Rows whose size differs from row to row, as the values of `dtype` (exact in float64)."""
     x = rng.normal(size=shape) * np.exp(0.7 * rng.normal(size=shape[:-1]))[..., None]
@@ -247,12 +251,9 @@ def test_chunks_and_decodes(Hq, Hkv, D, BS, dtype, W):
     assert cb.read_error_word(st.ws) == 0
 
 
-def launches(name):
-    return cb.launch_count(cb.kernel_names().index(name))
-
-
 @pytest.mark.parametrize("W", [0, 600])
-@pytest.mark.parametrize("Hq,Hkv,D,BS", [(32, 8, 128, 16), (16, 16, 128, 128), (32, 16, 64, 32), (16, 1, 64, 256)])
+@pytest.mark.parametrize("Hq,Hkv,D,BS", [(32, 8, 128, 16), (16, 16, 128, 128), (32, 16, 64, 32), (16, 1, 64, 256),
+                                         (32, 8, 128, 8)])
 def test_long_chunks_and_decodes(Hq, Hkv, D, BS, W):
     """Runs that are computed from bf16 copies of their pages, between decode rows."""
     st = Q8Step(spec_of([1, 530, 1, 257, 170], [90, 0, 400, 1333, 2128], num_q_heads=Hq, num_kv_heads=Hkv,
@@ -291,7 +292,7 @@ def test_few_chunks_behind_long_contexts(Hq, Hkv, D, BS, W, q, ctx):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("Hq,Hkv,D,BS", [(8, 2, 128, 1), (4, 4, 64, 8), (16, 1, 64, 2)])
+@pytest.mark.parametrize("Hq,Hkv,D,BS", [(8, 2, 128, 1), (4, 4, 64, 4), (16, 1, 64, 8), (16, 1, 64, 2)])
 def test_small_pages_run_on_the_portable_kernel(Hq, Hkv, D, BS, dtype):
     before = cb.launch_count(cb.kernel_names().index("portable_q8"))
     st = Q8Step(spec_of([1, 5, 0, 1], [40, 3, 2, 0], num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D,
@@ -299,6 +300,56 @@ def test_small_pages_run_on_the_portable_kernel(Hq, Hkv, D, BS, dtype):
     st.check(st.run())
     st.check_cache()
     assert cb.launch_count(cb.kernel_names().index("portable_q8")) == before + 1
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("W", [0, 21])
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (4, 4, 64), (32, 16, 64), (20, 10, 128), (32, 8, 128)])
+def test_pages_of_eight(Hq, Hkv, D, W, dtype):
+    """Key blocks of two pages: ends in the first and the second, new rows in either, values of
+    unattended slots, and a chunk."""
+    spec = spec_of([1, 5, 1, 1, 0, 1, 40, 1], [0, 3, 7, 8, 2, 23, 300, 1001], num_q_heads=Hq, num_kv_heads=Hkv,
+                   head_dim=D, block_size=8, dtype=dtype, sliding_window=W, seed=8)
+    st = Q8Step(spec, seed=5)
+    before = launches("portable_q8")
+    out = st.run()
+    st.check(out)
+    st.check_cache()
+    used = np.zeros(spec.num_blocks * 8, bool)
+    for r in range(spec.R):
+        first = max(0, int(spec.ctx_lens[r]) - W + 1) if W else 0
+        for p in range(first, int(spec.seq_lens[r])):
+            used[spec.block_table[r, p // 8] * 8 + p % 8] = True
+    keep = torch.from_numpy(used).cuda().view(spec.num_blocks, 8)
+    for i in range(4):
+        st.d[i][~keep] = 0x7F if i < 2 else 0xFF
+    assert torch.equal(st.run(), out)
+    assert cb.read_error_word(st.ws) == 0
+    assert launches("portable_q8") == before
+
+
+@pytest.mark.parametrize("q", [1, 3])
+def test_decode_rows_in_pages_of_eight(q):
+    """Decode rows alone (the new rows are written by the kernel that reads them), or runs."""
+    st = Q8Step(spec_of([q] * 9, [0, 1, 6, 7, 8, 15, 16, 700, 3001], block_size=8, seed=3), seed=4)
+    before = launches("portable_q8")
+    st.check(st.run())
+    st.check_cache()
+    assert launches("portable_q8") == before
+
+
+def test_a_bad_second_page_of_eight_reads_as_zeros():
+    spec = spec_of([1, 1], [100, 60], block_size=8, seed=2)
+    spec.block_table[0, 3] = spec.num_blocks + 5
+    spec.block_table[1, 5] = -1
+    st = Q8Step(spec, seed=1)
+    out = st.run()
+    assert cb.read_error_word(st.ws) == cb.CB_DEVERR_BLOCK_ID
+    for a in (st.k, st.v):
+        a[0] = np.concatenate([a[0], np.zeros_like(a[0][:1])])
+        a[1] = np.concatenate([a[1], np.full_like(a[1][:1], 127)])
+    spec.block_table[0, 3] = spec.block_table[1, 5] = spec.num_blocks
+    st.check(out)
 
 
 def test_portable_flag_agrees():
