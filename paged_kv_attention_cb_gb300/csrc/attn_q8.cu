@@ -1013,15 +1013,18 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
 // One CTA per (query row, KV head), for block sizes below 8 (a key block of the split kernel lies in
 // one page or two), odd KV head counts in pages of 8, and more KV heads than its ring's scales allow. Its warps take the row's
 // positions a few at a time in turn, each with a running (max, sum, output) in fp32 per query head of
-// the group, and join through shared memory at the end. Bound by the loads' latency, so a warp has
-// those of four positions in flight (one warp with one position: 2443 us for one request of 4000
-// positions in pages of 8, 32/8 heads).
+// the group, and join through shared memory at the end. Bound by the instructions of its shuffles and
+// exponentials on the row's SM: one request of 4000 positions in pages of 4, 32/8 heads, takes 174 us
+// (2443 with one warp and one position in flight), 64 of 128 .. 2048 positions 295.
 
-constexpr int kPortableWarps = 8;
-constexpr int kPortableKeys = 4;
+// Warps of a CTA, and positions a warp has in flight: as many as the group's queries and outputs
+// leave registers for.
+constexpr int portable_warps(int G) { return G <= 4 ? 16 : 8; }
+constexpr int portable_keys(int G) { return G <= 4 ? 8 : 4; }
 
 template <typename T, int VPT, int G>
-__global__ void __launch_bounds__(kPortableWarps * 32) q8_portable_kernel(StepArgs a, Q8Cache c) {
+__global__ void __launch_bounds__(portable_warps(G) * 32) q8_portable_kernel(StepArgs a, Q8Cache c) {
+  constexpr int kPortableWarps = portable_warps(G), kPortableKeys = portable_keys(G);
   constexpr int D = VPT * 32;
   __shared__ float sh_o[kPortableWarps][D];
   __shared__ float2 sh_ml[kPortableWarps];
@@ -1054,6 +1057,7 @@ __global__ void __launch_bounds__(kPortableWarps * 32) q8_portable_kernel(StepAr
     }
   }
   const int32_t* bt = a.block_table + (int64_t)r * a.bt_stride;
+  const int lg_block = __ffs(a.block_size) - 1;  // block sizes are powers of two
   for (int64_t p0 = (int64_t)first + warp * kPortableKeys; p0 <= last; p0 += kPortableWarps * kPortableKeys) {
     uint16_t kk[kPortableKeys][VPT / 2], xx[kPortableKeys][VPT / 2];
     int kc[kPortableKeys], vc[kPortableKeys];
@@ -1062,10 +1066,10 @@ __global__ void __launch_bounds__(kPortableWarps * 32) q8_portable_kernel(StepAr
 #pragma unroll
     for (int i = 0; i < kPortableKeys; ++i) {
       const int p = (int)min(p0 + i, (int64_t)last);
-      const int blk = __ldg(bt + bt_entry(p / a.block_size, a.ring_blocks));
+      const int blk = __ldg(bt + (p >> lg_block));
       ok[i] = blk >= 0 && blk < a.num_blocks;
       if (!ok[i] && lane == 0) record_error(a.error_word, CB_DEVERR_BLOCK_ID);
-      row[i] = ok[i] ? ((int64_t)blk * a.block_size + p % a.block_size) * Hkv + g : 0;
+      row[i] = ok[i] ? (((int64_t)blk << lg_block) + (p & (a.block_size - 1))) * Hkv + g : 0;
     }
 #pragma unroll
     for (int i = 0; i < kPortableKeys; ++i) {
@@ -1210,7 +1214,7 @@ template <typename T, int VPT>
 cudaError_t launch_portable_t(const StepArgs& a, const Q8Cache& c, cudaStream_t s) {
   const int64_t ctas = (int64_t)a.num_tokens * a.num_kv_heads;
   if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
-  const dim3 grid((unsigned)ctas), block(kPortableWarps * 32);
+  const dim3 grid((unsigned)ctas), block(portable_warps(a.num_q_heads / a.num_kv_heads) * 32);
   switch (a.num_q_heads / a.num_kv_heads) {
     case 1: return launch_pdl(kPortableQ8, q8_portable_kernel<T, VPT, 1>, grid, block, 0, s, a, c);
     case 2: return launch_pdl(kPortableQ8, q8_portable_kernel<T, VPT, 2>, grid, block, 0, s, a, c);
