@@ -1011,9 +1011,9 @@ q8_split_kernel(const __grid_constant__ CUtensorMap tmap_k,
 // ------------------------------------------------------------------ portable kernel
 //
 // One CTA per (query row, KV head), for block sizes below 8 (a key block of the split kernel lies in
-// one page or two), odd KV head counts in pages of 8, and more KV heads than its ring's scales allow. Its warps take the row's
-// positions a few at a time in turn, each with a running (max, sum, output) in fp32 per query head of
-// the group, and join through shared memory at the end. Bound by the instructions of its shuffles and
+// one page or two), odd KV head counts in pages of 8, and more KV heads than its ring's scales
+// allow. Its warps take the row's positions a few at a time in turn, each with a running (max, sum,
+// output) in fp32 per query head of the group, and join through shared memory at the end. Bound by the instructions of its shuffles and
 // exponentials on the row's SM: one request of 4000 positions in pages of 4, 32/8 heads, takes 174 us
 // (2443 with one warp and one position in flight), 64 of 128 .. 2048 positions 295.
 
